@@ -425,6 +425,55 @@ int mla_output_projection_prepared(const void* x, const void* wo_prepared, void*
                                    void* workspace, size_t workspace_bytes, int* d_status, cudaStream_t stream);
 
 /*
+ * The 8-bit latent cache.  The pages keep the latents in bf16; this cache
+ * holds them as E4M3 codes with one scale for each block of positions (the
+ * latent cache has one head, shared by all query heads), 640 bytes a position
+ * and its share of a scale instead of 1152:
+ *   kv_fp8   E4M3 codes [n_slots,S_max,512] (1 byte each)
+ *   pe       bf16 [n_slots,S_max,64], the rotated rotary key in units of the
+ *            block's scale
+ *   kv_scale f32 [n_slots, ceil(S_max/block)], positive and finite
+ *   block    positions that share a scale: a power of two, 1 to 128
+ * Position t of a slot stands for the latent s * e4m3(code) and the rotary key
+ * s * pe with s = kv_scale[slot, t / block]: one scale for the whole row, so
+ * that a score is s times one dot product.  kv_fp8, pe and kv_scale are device
+ * memory, 16-byte aligned.  The conventions above hold here too.
+ *
+ * mla_sparse_decode_fp8: the decode step, as mla_sparse_decode, over this
+ * cache.  Each of the R rows is one query:
+ *   cache_slot optional int32 [R] (16-byte aligned): row r reads slot
+ *            cache_slot[r], as in mla_sparse_prefill (a value outside
+ *            [0, n_slots) gives the row no valid position).  NULL: row r reads
+ *            slot r, and n_slots >= R
+ *   n_heads  heads of the call, 1 to 128, as in mla_sparse_decode_heads:
+ *            q_nope bf16 [R,n_heads,128], q_pe bf16 [R,n_heads,64], wkv_b bf16
+ *            [n_heads*256,512], out bf16 [R,n_heads,128], lse_out optional f32
+ *            [R,n_heads].  A call of at most 64 heads does half the attention
+ *            work of one of 128
+ *   workspace  mla_sparse_decode_fp8_workspace_size(R, K, S_max, n_heads)
+ * The scores are exact to f32 accumulation (q_lat bf16); the softmax weights
+ * enter the mix with 8 significant bits, as bf16 weights would, and the row
+ * sums are f32.
+ *
+ * mla_sparse_attend_fp8: steps "scores" .. "mix" alone, as mla_sparse_attend
+ * (o_part bf16 [R,n_split,n_heads,512], lse_part f32 [R,n_split,n_heads];
+ * q_lat bf16 [R,n_heads,512]); n_split must equal
+ * mla_num_splits_fp8(R, K, n_heads).
+ * All return an mla_status; the size functions return 0 for invalid sizes.
+ */
+int mla_num_splits_fp8(int R, int K, int n_heads);
+size_t mla_sparse_decode_fp8_workspace_size(int R, int K, int S_max, int n_heads);
+int mla_sparse_decode_fp8(const void* q_nope, const void* q_pe, const void* kv_fp8, const void* pe,
+                          const float* kv_scale, int block, const int32_t* cache_slot, const int32_t* end_pos,
+                          const int32_t* topk_idx, const void* wkv_b, float scale, void* out, int R, int K, int S_max,
+                          int n_slots, int n_heads, void* workspace, size_t workspace_bytes, float* lse_out,
+                          int* d_status, cudaStream_t stream);
+int mla_sparse_attend_fp8(const void* q_lat, const void* q_pe, const void* kv_fp8, const void* pe,
+                          const float* kv_scale, int block, const int32_t* cache_slot, const int32_t* end_pos,
+                          const int32_t* topk_idx, float scale, void* o_part, float* lse_part, int R, int K, int S_max,
+                          int n_slots, int n_heads, int n_split, int* d_status, cudaStream_t stream);
+
+/*
  * Self-test of the bounded waits every kernel relies on (no counterpart on the
  * pages): launches one CTA whose thread waits, through the kernels' own wait,
  * on a barrier that nothing arrives on.  After the wait limit (2 s) it must

@@ -30,7 +30,9 @@ EXPORTS = ("mla_status_string", "mla_num_splits", "mla_sparse_decode_workspace_s
            "mla_selftest_wait_timeout", "mla_check_topk_indices", "mla_set_index_checks",
            "mla_sparse_decode_heads_workspace_size", "mla_sparse_decode_heads",
            "mla_output_projection_shard_workspace_size", "mla_output_projection_shard", "mla_dequant_fp8_blocks",
-           "mla_prepare_wo", "mla_output_projection_prepared")
+           "mla_prepare_wo", "mla_output_projection_prepared",
+           "mla_num_splits_fp8", "mla_sparse_decode_fp8_workspace_size", "mla_sparse_decode_fp8",
+           "mla_sparse_attend_fp8")
 STATIC_SCRATCH_BYTES = 32 << 20  # MLA_STATIC_SCRATCH_BYTES
 
 _lib = None
@@ -101,6 +103,14 @@ def load_library():
     lib.mla_prepare_wo.argtypes = [p, ctypes.c_longlong, i, i, p, p]
     lib.mla_output_projection_prepared.restype = i
     lib.mla_output_projection_prepared.argtypes = [p, p, p, i, i, i, p, sz, p, p]
+    lib.mla_num_splits_fp8.restype = i
+    lib.mla_num_splits_fp8.argtypes = [i, i, i]
+    lib.mla_sparse_decode_fp8_workspace_size.restype = sz
+    lib.mla_sparse_decode_fp8_workspace_size.argtypes = [i, i, i, i]
+    lib.mla_sparse_decode_fp8.restype = i
+    lib.mla_sparse_decode_fp8.argtypes = [p, p, p, p, p, i, p, p, p, p, f, p, i, i, i, i, i, p, sz, p, p, p]
+    lib.mla_sparse_attend_fp8.restype = i
+    lib.mla_sparse_attend_fp8.argtypes = [p, p, p, p, p, i, p, p, p, f, p, p, i, i, i, i, i, i, p, p]
     lib.mla_selftest_wait_timeout.restype = i
     lib.mla_selftest_wait_timeout.argtypes = [p, p, p]
     _lib = lib
@@ -600,6 +610,127 @@ class Fp8Wkvb:
         if self._bf16 is None:
             self._bf16 = mla_dequant_fp8_blocks(self.w_fp8, self.scale, stream=stream)
         return self._bf16
+
+
+class Fp8Cache:
+    """A latent cache held in 8 bits: ``kv`` uint8 [n_slots, S_max, 512] (E4M3
+    codes), ``pe`` bf16 [n_slots, S_max, 64] and ``scale`` f32 [n_slots,
+    ceil(S_max / block)], one scale for each ``block`` positions (a power of
+    two, 1 to 128).  Position t of a slot stands for the latent s * e4m3(kv[t])
+    and the rotary key s * pe[t], s = scale[t // block]."""
+
+    def __init__(self, kv, pe, scale, block: int = 1):
+        if isinstance(block, bool) or not isinstance(block, int) or block not in (1, 2, 4, 8, 16, 32, 64, 128):
+            raise ValueError(f"block: expected a power of two from 1 to 128, got {block}")
+        if not isinstance(kv, torch.Tensor) or kv.dim() != 3:
+            raise ValueError("kv: expected a tensor [n_slots, S_max, 512]")
+        n_slots, S_max = kv.shape[0], kv.shape[1]
+        _check(kv, "kv", torch.uint8, (n_slots, S_max, D_LAT))
+        _check(pe, "pe", torch.bfloat16, (n_slots, S_max, D_ROPE))
+        _check(scale, "scale", torch.float32, (n_slots, (S_max + block - 1) // block))
+        self.kv, self.pe, self.scale, self.block = kv, pe, scale, block
+        self.n_slots, self.S_max = n_slots, S_max
+
+    @classmethod
+    def empty(cls, n_slots: int, S_max: int, block: int = 1, device="cuda"):
+        """A cache of zeros (its scales are 1)."""
+        return cls(torch.zeros((n_slots, S_max, D_LAT), dtype=torch.uint8, device=device),
+                   torch.zeros((n_slots, S_max, D_ROPE), dtype=torch.bfloat16, device=device),
+                   torch.ones((n_slots, (S_max + block - 1) // block), dtype=torch.float32, device=device), block)
+
+
+def _check_same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name}: on {t.device}, expected {device}")
+
+
+def num_splits_fp8(R: int, K: int, n_heads: int = H) -> int:
+    """mla_num_splits_fp8 for the current device (cached)."""
+    key = ("splits8", torch.cuda.current_device() if torch.cuda.is_available() else -1, R, K, n_heads)
+    v = _sizing_cache.get(key)
+    if v is None:
+        v = _sizing_cache[key] = int(load_library().mla_num_splits_fp8(R, K, n_heads))
+    return v
+
+
+def workspace_size_fp8(R: int, K: int, S_max: int, n_heads: int = H) -> int:
+    """mla_sparse_decode_fp8_workspace_size for the current device (cached)."""
+    key = ("ws8", torch.cuda.current_device() if torch.cuda.is_available() else -1, R, K, S_max, n_heads)
+    v = _sizing_cache.get(key)
+    if v is None:
+        v = _sizing_cache[key] = int(load_library().mla_sparse_decode_fp8_workspace_size(R, K, S_max, n_heads))
+    return v
+
+
+def mla_sparse_decode_fp8(q_nope, q_pe, cache: Fp8Cache, end_pos, topk_idx, wkv_b, scale, cache_slot=None, out=None,
+                          workspace=None, lse_out=None, d_status=None, stream=None):
+    """The decode step over an 8-bit cache: R rows (row r reads slot
+    cache_slot[r], or slot r) of n_heads heads each (q_nope bf16
+    [R, n_heads, 128], wkv_b bf16 [n_heads*256, 512]); returns ``out`` (bf16
+    [R, n_heads, 128])."""
+    lib = load_library()
+    R, n_heads = q_nope.shape[0], q_nope.shape[1]
+    K, S_max = topk_idx.shape[1], cache.S_max
+    bf = torch.bfloat16
+    _check(q_nope, "q_nope", bf, (R, n_heads, D_NOPE))
+    _check(q_pe, "q_pe", bf, (R, n_heads, D_ROPE))
+    _check(end_pos, "end_pos", torch.int32, (R,))
+    _check(topk_idx, "topk_idx", torch.int32, (R, K))
+    _check(wkv_b, "wkv_b", bf, (n_heads * (D_NOPE + D_V), D_LAT))
+    if cache_slot is not None:
+        _check(cache_slot, "cache_slot", torch.int32, (R,))
+    if out is None:
+        out = torch.empty((R, n_heads, D_V), dtype=bf, device=q_nope.device)
+    _check(out, "out", bf, (R, n_heads, D_V))
+    if lse_out is not None:
+        _check(lse_out, "lse_out", torch.float32, (R, n_heads))
+    if d_status is not None:
+        _check(d_status, "d_status", torch.int32, (1,))
+    if workspace is None:
+        need = workspace_size_fp8(R, K, S_max, n_heads)
+        if need == 0:
+            raise MLAError(1, "mla_sparse_decode_fp8")
+        workspace = torch.empty(need, dtype=torch.uint8, device=q_nope.device)
+    _check(workspace, "workspace", torch.uint8)
+    _check_same_device(q_nope.device, q_pe=q_pe, cache=cache.kv, end_pos=end_pos, topk_idx=topk_idx, wkv_b=wkv_b,
+                       cache_slot=cache_slot, out=out, workspace=workspace, lse_out=lse_out, d_status=d_status)
+    rc = lib.mla_sparse_decode_fp8(_ptr(q_nope), _ptr(q_pe), _ptr(cache.kv), _ptr(cache.pe), _ptr(cache.scale),
+                                   cache.block, _ptr(cache_slot), _ptr(end_pos), _ptr(topk_idx), _ptr(wkv_b),
+                                   float(scale), _ptr(out), R, K, S_max, cache.n_slots, n_heads, _ptr(workspace),
+                                   workspace.numel(), _ptr(lse_out), _ptr(d_status), _stream(stream))
+    _raise(rc, "mla_sparse_decode_fp8")
+    return out
+
+
+def mla_sparse_attend_fp8(q_lat, q_pe, cache: Fp8Cache, end_pos, topk_idx, scale, cache_slot=None, o_part=None,
+                          lse_part=None, d_status=None, stream=None):
+    """Per-split outputs over an 8-bit cache; returns (o_part bf16
+    [R, S, n_heads, 512], lse_part f32 [R, S, n_heads])."""
+    lib = load_library()
+    R, n_heads, K = q_lat.shape[0], q_lat.shape[1], topk_idx.shape[1]
+    n_split = num_splits_fp8(R, K, n_heads)
+    bf = torch.bfloat16
+    _check(q_lat, "q_lat", bf, (R, n_heads, D_LAT))
+    _check(q_pe, "q_pe", bf, (R, n_heads, D_ROPE))
+    _check(end_pos, "end_pos", torch.int32, (R,))
+    _check(topk_idx, "topk_idx", torch.int32, (R, K))
+    if cache_slot is not None:
+        _check(cache_slot, "cache_slot", torch.int32, (R,))
+    if o_part is None:
+        o_part = torch.empty((R, n_split, n_heads, D_LAT), dtype=bf, device=q_lat.device)
+    if lse_part is None:
+        lse_part = torch.empty((R, n_split, n_heads), dtype=torch.float32, device=q_lat.device)
+    _check(o_part, "o_part", bf, (R, n_split, n_heads, D_LAT))
+    _check(lse_part, "lse_part", torch.float32, (R, n_split, n_heads))
+    _check_same_device(q_lat.device, q_pe=q_pe, cache=cache.kv, end_pos=end_pos, topk_idx=topk_idx,
+                       cache_slot=cache_slot, o_part=o_part, lse_part=lse_part, d_status=d_status)
+    rc = lib.mla_sparse_attend_fp8(_ptr(q_lat), _ptr(q_pe), _ptr(cache.kv), _ptr(cache.pe), _ptr(cache.scale),
+                                   cache.block, _ptr(cache_slot), _ptr(end_pos), _ptr(topk_idx), float(scale),
+                                   _ptr(o_part), _ptr(lse_part), R, K, cache.S_max, cache.n_slots, n_heads,
+                                   n_split, _ptr(d_status), _stream(stream))
+    _raise(rc, "mla_sparse_attend_fp8")
+    return o_part, lse_part
 
 
 def host_input_buffer(B: int, K: int, S_max: int):

@@ -11,6 +11,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "attend_fp8.cuh"
 #include "dequant.cuh"
 #include "index_check.cuh"
 #include "kernels.cuh"
@@ -56,6 +57,7 @@ int current_device(DeviceInfo** info) {
     if (d.sm100) {
       if (cudaFuncSetAttribute(absorb_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAbsorbSmemBytes) != cudaSuccess ||
           cudaFuncSetAttribute(sparse_attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttendSmemBytes) != cudaSuccess ||
+          cudaFuncSetAttribute(sparse_attend_fp8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kF8SmemBytes) != cudaSuccess ||
           cudaFuncSetAttribute(combine_value_up_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCombineSmemBytes) != cudaSuccess ||
           cudaFuncSetAttribute(projection_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, proj_smem_max()) != cudaSuccess ||
           cudaFuncSetAttribute(check_indices_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -216,6 +218,30 @@ void plan_splits(int B, int K, int sm_count, int* n_split, int* span) {
   *n_split = ceil_div(K, sp);
 }
 
+// The same over the 8-bit cache: one CTA per (row, split, group of 64 heads),
+// splits of whole 128-slot tiles.
+int fp8_groups(int n_heads) { return ceil_div(n_heads, kF8Heads); }
+
+void plan_splits_fp8(int R, int K, int n_heads, int sm_count, int* n_split, int* span) {
+  const int tiles = ceil_div(K, kF8Nt);
+  long long want = sm_count / ((long long)R * fp8_groups(n_heads));
+  if (want < 1) want = 1;
+  if (want > tiles) want = tiles;
+  if (want > kCombineMaxSplits) want = kCombineMaxSplits;
+  const int sp = ceil_div(tiles, (int)want) * kF8Nt;
+  *span = sp;
+  *n_split = ceil_div(K, sp);
+}
+
+constexpr int kFp8MaxBlock = 128;
+
+// log2 of the positions that share a scale, or -1.
+int block_shift(int block) {
+  for (int s = 0; (1 << s) <= kFp8MaxBlock; ++s)
+    if (block == 1 << s) return s;
+  return -1;
+}
+
 constexpr int kProjMaxDim = 1 << 16;
 
 bool proj_sizes_ok(int B, int dim) {
@@ -321,6 +347,22 @@ int launch_attend(const void* q_lat, const void* q_pe, const void* kv_cache, con
                    static_cast<const __nv_bfloat16*>(kv_cache), static_cast<const __nv_bfloat16*>(pe_cache), end_pos,
                    topk_idx, scale, o_part, lse_part, K, S_max, n_split, span,
                    static_cast<const __nv_bfloat16*>(w_next), cache_slot, n_slots, n_heads, d_status);
+}
+
+int launch_attend_fp8(const void* q_lat, const void* q_pe, const void* kv_fp8, const void* pe, const float* kv_scale,
+                      int shift, const int32_t* cache_slot, const int32_t* end_pos, const int32_t* topk_idx,
+                      float scale, void* o_part, float* lse_part, int R, int K, int S_max, int n_slots, int n_heads,
+                      int n_split, int span, const void* w_next, int* d_status, cudaStream_t stream, bool pdl) {
+  const int groups = fp8_groups(n_heads);
+  const long long ctas = (long long)R * n_split * groups;
+  if (ctas > 0x7fffffffLL) return MLA_ERR_INVALID_ARG;
+  const int n_blocks = ((S_max - 1) >> shift) + 1;
+  return launch_ex(sparse_attend_fp8_kernel, dim3((unsigned)ctas), dim3(kF8Threads), kF8SmemBytes, stream, pdl,
+                   static_cast<const __nv_bfloat16*>(q_lat), static_cast<const __nv_bfloat16*>(q_pe),
+                   static_cast<const uint8_t*>(kv_fp8), static_cast<const __nv_bfloat16*>(pe), kv_scale, shift,
+                   n_blocks, end_pos, topk_idx, scale, static_cast<__nv_bfloat16*>(o_part), lse_part, K, S_max,
+                   n_split, span, static_cast<const __nv_bfloat16*>(w_next), cache_slot, n_slots, n_heads, groups,
+                   d_status);
 }
 
 int launch_combine(const void* o_part, const float* lse_part, const void* wkv_b, void* out, float* lse_out, int B,
@@ -568,6 +610,95 @@ extern "C" int mla_sparse_decode_heads(const void* q_nope, const void* q_pe, con
   if (n_heads < 1 || n_heads > kH) return MLA_ERR_INVALID_ARG;
   return run_rows(q_nope, q_pe, kv_cache, pe_cache, end_pos, topk_idx, wkv_b, scale, out, B, K, S_max, nullptr, B,
                   workspace, workspace_bytes, lse_out, d_status, stream, n_heads);
+}
+
+// ---------------------------------------------------------------- 8-bit cache
+namespace {
+// What every entry point over the 8-bit cache asks of it.
+bool fp8_cache_ok(const void* kv_fp8, const void* pe, const float* kv_scale, int block, int S_max, int n_slots) {
+  return kv_fp8 && pe && kv_scale && aligned16(kv_fp8) && aligned16(pe) && aligned16(kv_scale) &&
+         block_shift(block) >= 0 && S_max >= 1 && n_slots >= 1;
+}
+
+// A row without a slot of its own reads the slot of its number.
+bool slots_ok(const int32_t* cache_slot, int R, int n_slots) {
+  return cache_slot ? aligned16(cache_slot) : n_slots >= R;
+}
+}  // namespace
+
+extern "C" int mla_num_splits_fp8(int R, int K, int n_heads) {
+  if (!sizes_ok(R, K, 1) || n_heads < 1 || n_heads > kH) return 0;
+  int n_split = 0, span = 0;
+  plan_splits_fp8(R, K, n_heads, planning_sm_count(), &n_split, &span);
+  return n_split;
+}
+
+extern "C" size_t mla_sparse_decode_fp8_workspace_size(int R, int K, int S_max, int n_heads) {
+  if (!sizes_ok(R, K, S_max) || n_heads < 1 || n_heads > kH) return 0;
+  int n_split = 0, span = 0;
+  plan_splits_fp8(R, K, n_heads, planning_sm_count(), &n_split, &span);
+  return workspace_layout(R, n_split, n_heads).total;
+}
+
+extern "C" int mla_sparse_attend_fp8(const void* q_lat, const void* q_pe, const void* kv_fp8, const void* pe,
+                                     const float* kv_scale, int block, const int32_t* cache_slot,
+                                     const int32_t* end_pos, const int32_t* topk_idx, float scale, void* o_part,
+                                     float* lse_part, int R, int K, int S_max, int n_slots, int n_heads, int n_split,
+                                     int* d_status, cudaStream_t stream) {
+  const void* ptrs[] = {q_lat, q_pe, end_pos, topk_idx, o_part, lse_part};
+  for (const void* p : ptrs)
+    if (!p || !aligned16(p)) return MLA_ERR_INVALID_ARG;
+  if (!fp8_cache_ok(kv_fp8, pe, kv_scale, block, S_max, n_slots) || !slots_ok(cache_slot, R, n_slots))
+    return MLA_ERR_INVALID_ARG;
+  if (d_status && (reinterpret_cast<uintptr_t>(d_status) & 3u)) return MLA_ERR_INVALID_ARG;
+  if (!sizes_ok(R, K, S_max) || n_heads < 1 || n_heads > kH || !std::isfinite(scale)) return MLA_ERR_INVALID_ARG;
+  DeviceInfo* info = nullptr;
+  int rc = prepare(&info);
+  if (rc != MLA_OK) return rc;
+  int want = 0, span = 0;
+  plan_splits_fp8(R, K, n_heads, info->sm_count, &want, &span);
+  if (n_split != want) return MLA_ERR_INVALID_ARG;
+  return launch_attend_fp8(q_lat, q_pe, kv_fp8, pe, kv_scale, block_shift(block), cache_slot, end_pos, topk_idx,
+                           scale, o_part, lse_part, R, K, S_max, n_slots, n_heads, n_split, span, nullptr, d_status,
+                           stream, false);
+}
+
+// The decode step over the 8-bit cache (see the header): absorption and
+// value-up as in mla_sparse_decode, the attention of attend_fp8.cuh between.
+extern "C" int mla_sparse_decode_fp8(const void* q_nope, const void* q_pe, const void* kv_fp8, const void* pe,
+                                     const float* kv_scale, int block, const int32_t* cache_slot,
+                                     const int32_t* end_pos, const int32_t* topk_idx, const void* wkv_b, float scale,
+                                     void* out, int R, int K, int S_max, int n_slots, int n_heads, void* workspace,
+                                     size_t workspace_bytes, float* lse_out, int* d_status, cudaStream_t stream) {
+  const void* ptrs[] = {q_nope, q_pe, end_pos, topk_idx, wkv_b, out};
+  for (const void* p : ptrs)
+    if (!p || !aligned16(p)) return MLA_ERR_INVALID_ARG;
+  if (!fp8_cache_ok(kv_fp8, pe, kv_scale, block, S_max, n_slots) || !slots_ok(cache_slot, R, n_slots))
+    return MLA_ERR_INVALID_ARG;
+  if (lse_out && (reinterpret_cast<uintptr_t>(lse_out) & 3u)) return MLA_ERR_INVALID_ARG;
+  if (d_status && (reinterpret_cast<uintptr_t>(d_status) & 3u)) return MLA_ERR_INVALID_ARG;
+  if (!sizes_ok(R, K, S_max) || n_heads < 1 || n_heads > kH || !std::isfinite(scale)) return MLA_ERR_INVALID_ARG;
+  DeviceInfo* info = nullptr;
+  int rc = prepare(&info);
+  if (rc != MLA_OK) return rc;
+  int n_split = 0, span = 0;
+  plan_splits_fp8(R, K, n_heads, info->sm_count, &n_split, &span);
+  const WorkspaceLayout wl = workspace_layout(R, n_split, n_heads);
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < wl.total)
+    return MLA_ERR_WORKSPACE;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  void* q_lat = ws + wl.q_lat;
+  void* o_part = ws + wl.o_part;
+  float* lse_part = reinterpret_cast<float*>(ws + wl.lse_part);
+  if (d_status && g_index_checks.load(std::memory_order_relaxed) &&
+      (rc = launch_check_indices(end_pos, topk_idx, R, K, S_max, d_status, nullptr, stream)) != MLA_OK)
+    return rc;
+  if ((rc = launch_absorb(q_nope, wkv_b, q_lat, R, d_status, stream, n_heads)) != MLA_OK) return rc;
+  if ((rc = launch_attend_fp8(q_lat, q_pe, kv_fp8, pe, kv_scale, block_shift(block), cache_slot, end_pos, topk_idx,
+                              scale, o_part, lse_part, R, K, S_max, n_slots, n_heads, n_split, span, wkv_b, d_status,
+                              stream, true)) != MLA_OK)
+    return rc;
+  return launch_combine(o_part, lse_part, wkv_b, out, lse_out, R, n_split, d_status, stream, true, n_heads);
 }
 
 // fp8 block dequantisation (see the header).
