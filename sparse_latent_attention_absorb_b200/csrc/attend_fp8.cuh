@@ -25,15 +25,28 @@ namespace mla {
 // what one bf16 product costs, and the codes go to the tensor cores as they
 // lie in the cache, with no conversion and at half of bf16's shared memory.
 
-// Two floats of magnitude <= 448 to their E4M3 pair (round to nearest even)
-// and back.
-__device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+//
+// An fp16 number f of magnitude below 1.8 has E4M3's exponent field for the
+// value 2^8 f, subnormals included, so rounding 2^8 f to E4M3 is rounding f's
+// bits to a multiple of 2^7 and taking seven of them.  (The conversion
+// instructions do a quarter of the integer units' rate: a tile's P took 1020
+// cycles with them, 600 so.)  Ties go away from zero.
+//
+// Two fp16 numbers: their first limbs as fp16 values, and what those leave.
+__device__ __forceinline__ uint32_t limb_first(uint32_t f16x2) { return f16x2 + 0x00400040u; }  // bits 7.. are the limb
+__device__ __forceinline__ __half2 limb_rest(uint32_t f16x2, uint32_t first) {
+  const uint32_t cut = first & 0xbf80bf80u;
+  return __hsub2(*reinterpret_cast<const __half2*>(&f16x2), *reinterpret_cast<const __half2*>(&cut));
 }
-__device__ __forceinline__ float2 unpack_e4m3x2(uint32_t v) {
-  const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v), __NV_E4M3);
-  return __half22float2(*reinterpret_cast<const __half2*>(&r));
+// The E4M3 bytes of four rounded fp16 numbers (sign, then bits 13..7 of each).
+__device__ __forceinline__ uint32_t limb_bytes(uint32_t a, uint32_t b) {
+  const uint32_t u = (a & 0x80008000u) | ((a << 1) & 0x7f007f00u), v = (b & 0x80008000u) | ((b << 1) & 0x7f007f00u);
+  return __byte_perm(u, v, 0x7531);
 }
+__device__ __forceinline__ uint32_t limb_bytes_positive(uint32_t a, uint32_t b) {
+  return __byte_perm(a << 1, b << 1, 0x7531);
+}
+__device__ __forceinline__ uint32_t half2_bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 
 // Exponent e with |amax| 2^e in (224, 448] (0 for amax = 0).
 __device__ __forceinline__ int limb_exponent(float amax) {
@@ -45,146 +58,168 @@ __device__ __forceinline__ int limb_exponent(float amax) {
 }
 __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }  // |e| <= 126
 
-// Eight bf16 numbers (one 16-byte load) times 2^e as limbs: x 2^e = hi + lo / 16.
-// The second limb is scaled by 16 so that it keeps its bits however small x
-// is.  An infinite or NaN x gives a NaN second limb.
+// Four bf16 query factors x as limbs: x 2^e = hi + lo / 16, `mul` = 2^(e - 8).
+// The second limb is scaled by 16 so that it keeps its bits however small x is:
+// a bf16 x is met exactly (4 + 4 signed bits) down to 2^-17 of the largest.
 constexpr float kLimbLo = 1.f / 16.f;
-__device__ __forceinline__ void limbs8(const uint4& raw, float mul, uint2* hi, uint2* lo) {
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-  uint32_t h[4], l[4];
+__device__ __forceinline__ void limbs4(uint32_t x01, uint32_t x23, float mul, uint32_t* hi, uint32_t* lo) {
+  uint32_t first[2], rest[2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float a = __uint_as_float(w[i] << 16) * mul, b = __uint_as_float(w[i] & 0xffff0000u) * mul;
-    h[i] = pack_e4m3x2(a, b);
-    const float2 r = unpack_e4m3x2(h[i]);
-    l[i] = pack_e4m3x2(fmaf(a, 0.f, (a - r.x) * 16.f), fmaf(b, 0.f, (b - r.y) * 16.f));
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t x = i ? x23 : x01;
+    const uint32_t f = half2_bits(__floats2half2_rn(__uint_as_float(x << 16) * mul, __uint_as_float(x & 0xffff0000u) * mul));
+    first[i] = limb_first(f);
+    rest[i] = limb_first(half2_bits(__hmul2(limb_rest(f, first[i]), __float2half2_rn(16.f))));
   }
-  *hi = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
-  *lo = make_uint2(l[0] | (l[1] << 16), l[2] | (l[3] << 16));
+  *hi = limb_bytes(first[0], first[1]);
+  *lo = limb_bytes(rest[0], rest[1]);
 }
 
-// The largest finite magnitude among eight bf16 numbers.
-__device__ __forceinline__ float amax8(const uint4& raw) {
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t a = w[i] & 0x7fffu, b = (w[i] >> 16) & 0x7fffu;
-    if (a < 0x7f80u) m = max(m, a);
-    if (b < 0x7f80u) m = max(m, b);
-  }
-  return __uint_as_float(m << 16);
-}
-
-// Thirty-two values of each lane, reduced over the lanes: lane i returns the
-// result of value i (31 exchanges instead of 160).
-template <typename Op>
-__device__ __forceinline__ float reduce_transposed(float (&v)[32], int lane, Op op) {
-#pragma unroll
-  for (int s = 16; s >= 1; s >>= 1) {
-    const bool up = (lane & s) != 0;
-#pragma unroll
-    for (int i = 0; i < s; ++i) {
-      const float keep = up ? v[i + s] : v[i], send = up ? v[i] : v[i + s];
-      v[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, s));
-    }
-  }
-  return v[0];
-}
+// The magnitudes' bits of two bf16 numbers, each the larger of m's and x's.
+__device__ __forceinline__ uint32_t amax2(uint32_t m, uint32_t x) { return __vmaxu2(m, x & 0x7fff7fffu); }
 
 // =============================================================================
 // sparse_attend_fp8_kernel
 //
-// One CTA per (row, key split, group of 64 heads), no cluster: everything is
-// transposed, positions on the MMA's 128 rows, so that 64 heads and all 512
-// latent columns fit one SM's tensor memory and no score crosses SMs:
-//   S^T[t, h] = code_t . q_h      M = 128 positions, N = 64 hi + 64 lo limbs
-//                                 of the query (E4M3, K-major both), plus the
-//                                 bf16 rotary product into the hi columns;
-//   O^T[c, h] += code_t[c] P[t, h]  M = 128 latent columns (four blocks),
-//                                 N = 64, the tile's codes read M-major from
-//                                 the same shared memory, P as two limbs.
-// A softmax thread holds one position (TMEM lane) and 32 heads.  Its scale
-// enters as two scalars: y = s_t scale (S_hi + S_lo / 16) + log2 s_t is the
-// log2 weight of the position's *codes*, P = 2^(y - m_h), and the row sum adds
-// P / s_t.  m_h is the largest y of some tile plus a margin; it moves only
-// when P would leave E4M3's range (a vote among the CTA's softmax warps, one
-// barrier a tile), and then O is rescaled in place.
+// Per tile of 128 positions:
+//   S[r, t]      = q_r . code_t   M = 128 rows: the hi and lo limbs of 64 heads'
+//                                 queries (TMEM; 16 heads' hi rows, then their
+//                                 lo rows, in every 32 lanes), N = 128 positions
+//                                 (K-major, as gathered), plus the bf16 rotary
+//                                 product into the hi rows.  S_hi + S_lo / 16
+//                                 meets in one shuffle across half a warp;
+//   y[h, t]      = scale s_t S + log2 s_t, the log2 weight of position t's codes;
+//   P[h, t]      = 2^(y - m_h), row sum += P / s_t;
+//   O^T[c, h]   += code_t[c] P[h, t]   M = 128 latent columns, N = the heads, the
+//                                 same codes read M-major, P as two limbs one
+//                                 after the other.
+// Every score is formed whole in one SM and in f32.  O is kept transposed so
+// that P is the N operand: as rows, P's two limbs would need two sets of
+// accumulators.
 //
-// Shared memory: two 64 KB stages of 128 positions x 512 codes (four 128-byte
-// swizzled blocks), the query's limbs (64 KB) and rotary part (8 KB), P
-// (16 KB).  A tile's rotary rows borrow the stage's block 0: they are the
-// first to be multiplied, and the codes of columns 0..127 follow them.
+// Pair (more than 64 heads): a 2-CTA cluster per (row, split).  CTA r owns 64
+// heads of QK and softmax, and latent columns 256 r.. of O for all heads, so it
+// sends its P to the peer (bulk copies: the softmax warps go on meanwhile).  N
+// is 128 in both products: an MMA of N = 64 takes 60 cycles, one of N = 128
+// takes 65.  Only P crosses SMs; the rows are read by both, once from L2.
+// Single (at most 64 heads): one CTA per (row, split) owns all 512 columns.
 //
-// Warps (448 threads): 0-7 softmax (warp w: positions 32 (w % 4).., heads
-// 32 (w / 4)..), 8 QK issue, 9 TMEM and PV issue, 10-13 gather (32 positions
-// of every tile each).
+// m_h is the largest y of some tile plus a margin, and moves only when P would
+// leave E4M3's range; the softmax warps then rescale the columns of O of the
+// heads it moved for between two PVs, in both CTAs of a pair (which tell each
+// other as soon as they know, while P is being formed).
+//
+// Shared memory: blocks of 16 KB (128 positions x 128 bytes, 128-byte swizzle).
+//   Pair:   a ring of four for what only QK reads (rotary rows, the peer's
+//           columns), three stages of the CTA's own columns (two blocks each,
+//           held until PV has read them), P (two limbs of 128 heads).
+//   Single: a ring of two for the rotary rows, two stages of four blocks, P.
+// The tile's time is set by how far the gather runs ahead: with two stages and
+// one set of the peer's columns it took 4000 cycles, of about 2400 of MMA.
+//
+// Warps (480 threads): 0-7 softmax (warp w: TMEM lanes 32 (w % 4).., positions
+// 64 (w / 4)..), 8-11 gather (one on each sub-partition of the SM: two warps on
+// two of them took 4900 cycles a tile), 12 query load and QK issue, 13 TMEM, PV
+// issue and pushes, 14 positions, scales and L2 prefetch.
 // =============================================================================
-constexpr int kF8Heads = 64;                        // heads of a CTA
-constexpr int kF8Nt = 128;                          // positions of a tile
-constexpr int kF8Block = kF8Nt * 128;               // 128 codes of every position: 16 KB
-constexpr int kF8StageBytes = 4 * kF8Block;
-constexpr int kF8QBytes = 4 * 2 * kF8Heads * 128;   // per 128 columns: 64 hi rows, 64 lo rows
-constexpr int kF8PBytes = kF8Nt * kF8Heads;         // one limb of P
-constexpr int kF8QpeBytes = kF8Heads * 128;
-constexpr int kF8OffQ = 2 * kF8StageBytes;
-constexpr int kF8OffP = kF8OffQ + kF8QBytes;
-constexpr int kF8OffQpe = kF8OffP + 2 * kF8PBytes;
-constexpr int kF8OffScale = kF8OffQpe + kF8QpeBytes;         // f32 [2][128]: the positions' scales, 0 = masked
-constexpr int kF8OffRed = kF8OffScale + 2 * kF8Nt * 4;       // f32 [4][64]
-constexpr int kF8OffRef = kF8OffRed + 4 * kF8Heads * 4;      // f32 [64]: m_h
-constexpr int kF8OffAlpha = kF8OffRef + kF8Heads * 4;        // f32 [64]
-constexpr int kF8OffBar = kF8OffAlpha + kF8Heads * 4;
+constexpr int kF8Heads = 64;           // heads of a CTA's QK and softmax
+constexpr int kF8Nt = 128;             // positions of a tile
+constexpr int kF8Block = kF8Nt * 128;  // 16 KB
+__host__ __device__ constexpr int f8_ring(bool pair) { return pair ? 4 : 2; }         // blocks that only QK reads
+__host__ __device__ constexpr int f8_ring_per(bool pair) { return pair ? 3 : 1; }     // of them a tile
+__host__ __device__ constexpr int f8_stages(bool pair) { return pair ? 3 : 2; }       // stages of own columns
+__host__ __device__ constexpr int f8_own(bool pair) { return pair ? 2 : 4; }          // blocks of a stage
+__host__ __device__ constexpr int f8_own_at(bool pair, int st, int i) { return (f8_ring(pair) + f8_own(pair) * st + i) * kF8Block; }
+constexpr int kF8OffP = 10 * kF8Block;                       // hi limbs, then lo limbs
+constexpr int kF8OffQpe = kF8OffP + 2 * kF8Block;            // 128 rows (the lo rows are zero)
+constexpr int kF8OffKey = kF8OffQpe + kF8Block;              // f32 [4][3][128]: what a position's scale enters by
+constexpr int kF8OffPos = kF8OffKey + 4 * 3 * kF8Nt * 4;     // int [4][128]: a tile's positions, -1 = masked
+constexpr int kF8OffRed = kF8OffPos + 4 * kF8Nt * 4;         // f32 [2][2][64]
+constexpr int kF8OffMove = kF8OffRed + 2 * 2 * kF8Heads * 4; // F8Move [2][2]
+constexpr int kF8OffFin = kF8OffMove + 2 * 2 * 272;          // f32 [128]: one over the row sums
+constexpr int kF8OffBar = kF8OffFin + kH * 4;
 constexpr int kF8SmemBytes = kF8OffBar + 512 + kSmemAlignPad;
 constexpr int kF8SoftmaxWarps = 8;
-constexpr int kF8QkWarp = 8, kF8PvWarp = 9, kF8GatherWarp = 10, kF8GatherWarps = 4;
-constexpr int kF8Threads = 32 * (kF8GatherWarp + kF8GatherWarps);
-constexpr uint32_t kF8ColS = 0;    // two score buffers of 64 hi + 64 lo columns
-constexpr uint32_t kF8ColO = 256;  // four blocks of 64 columns
-// P is formed in fp16 at 2^-8 of its E4M3 value (fp16's exponent field is then
-// E4M3's, so a limb is a byte of the fp16 number).  A new m_h puts the largest
-// P of its tile at 2^-3 (2^5 in E4M3); a later one may reach 2^0.75 (430 in
-// E4M3, of at most 448) before m_h has to move.
-constexpr float kF8RefMargin = 3.0f;
-constexpr float kF8RefLimit = 0.75f;
+constexpr int kF8GatherWarp = 8, kF8GatherWarps = 4, kF8QkWarp = 12, kF8PvWarp = 13, kF8IndexWarp = 14;
+constexpr int kF8Threads = 480;
+constexpr uint32_t kF8ColS = 0;    // scores: 128 columns
+constexpr uint32_t kF8ColQ = 128;  // the query's limbs: 128 columns of four codes
+constexpr uint32_t kF8ColO = 256;  // pair: 2 blocks of 128 heads; single: 4 blocks of 64
+// P is formed in fp16 at 2^-8 of its E4M3 value.  A new m_h puts the largest P
+// of its tile at 2^3 (in E4M3); a later one may reach 2^8.75 = 430 (E4M3's
+// largest value is 448) before m_h has to move.  E4M3 resolves 2^-9: more room
+// above costs small weights their bits (the mix of 2048 positions of
+// unit-variance scores is off by 5.8e-4 at 2^5, 8.0e-4 at 2^3, 1.3e-3 at 2^2),
+// less of it moves m_h more often (13, none and none of 15 tiles had a head
+// that moved, at 2^5, 2^3 and 2^2).
+constexpr float kF8RefMargin = 8.0f - 3.0f;
+constexpr float kF8RefLimit = 8.75f - 8.0f;
 constexpr float kF8NoRef = -1e30f;  // m_h before any position counted
+// How a tile moves the references of a CTA's 64 heads.
+struct F8Move {
+  float factor[kF8Heads];  // O's columns are multiplied by it
+  uint32_t moved[4];       // the heads whose factor is not 1, 16 a word
+};
+static_assert(sizeof(F8Move) == 272, "kF8OffFin");
+// A limb of a CTA's P: 64 heads x 128 positions (K-major, 128-byte swizzle).  A
+// CTA of a pair sends its peer both limbs and its F8Move.
+constexpr int kF8Limb = kF8Nt * kF8Heads;
 static_assert(kF8SmemBytes <= 232448, "shared memory");
-static_assert(kF8OffQ % 1024 == 0 && kF8OffP % 1024 == 0 && kF8OffQpe % 1024 == 0, "swizzle atoms");
-static_assert(kF8GatherWarps * 32 == kF8Nt, "a gather lane per position");
+static_assert(4 * kF8GatherWarps % 8 == 0, "a gather warp's rows share their swizzle");
+static_assert(f8_ring(true) + f8_stages(true) * f8_own(true) == 10 && f8_ring(false) + f8_stages(false) * f8_own(false) == 10, "blocks");
 
 struct F8Bars {
-  uint64_t q_full;       // 8 softmax warps: the query's limbs are in shared memory
-  uint64_t full[2][5];   // 128 gather lanes: block i of the stage (4: the rotary rows) has landed
-  uint64_t empty[2][4];  // MMA commit: PV has read block i
-  uint64_t pe_done[2];   // MMA commit: the rotary product has read block 0
-  uint64_t sc_full[2];   // 4 gather warps: the positions' scales
-  uint64_t s_full[2];    // MMA commit: scores of the buffer
-  uint64_t s_empty[2];   // 8 softmax warps: scores read
-  uint64_t p_full;       // 8 softmax warps: P written
-  uint64_t p_free;       // MMA commit: PV done (P free, O stable)
+  uint64_t q_tma;         // the query's boxes landed
+  uint64_t q_full;        // 8 softmax warps: the query's limbs are in TMEM
+  uint64_t ring_full[2];  // the gather lanes, once a block: the tile's ring blocks have landed
+  uint64_t ring_empty[4]; // MMA commit: QK has read it
+  uint64_t own_full[3];   // the same of its stage
+  uint64_t own_empty[3];  // MMA commit: PV has read the stage
+  uint64_t tile_full[4];  // a tile's positions and scales
+  uint64_t tile_done[4];  // MMA commit: its PV is done
+  uint64_t s_full;        // MMA commit: scores ready
+  uint64_t s_empty;       // 8 softmax warps: scores read
+  uint64_t p_own;         // 8 softmax warps: the CTA's part of P written
+  uint64_t p_hi, p_lo;    // pair: one arming arrival and the peer's limb
+  uint64_t moves[2];      // pair: one arming arrival and the peer's F8Move
+  uint64_t p_free;        // MMA commit of the CTA's (pair: and the peer's) PV: P free, pushes gone, O stable
   uint32_t tmem_addr;
   int abort_flag;
 };
 static_assert(sizeof(F8Bars) <= 512, "barrier block");
 
+__device__ __forceinline__ void st_shared_v4(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+
+template <bool kPair>
 __global__ void __launch_bounds__(kF8Threads, 1)
-sparse_attend_fp8_kernel(const __nv_bfloat16* __restrict__ q_lat, const __nv_bfloat16* __restrict__ q_pe,
+sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __nv_bfloat16* __restrict__ q_pe,
                          const uint8_t* __restrict__ kv8, const __nv_bfloat16* __restrict__ pe8,
                          const float* __restrict__ kv_scale, int block_shift, int n_blocks,
                          const int32_t* __restrict__ end_pos, const int32_t* __restrict__ topk_idx, float scale,
                          __nv_bfloat16* __restrict__ o_part, float* __restrict__ lse_part, int K, int S_max,
                          int n_split, int span, const __nv_bfloat16* __restrict__ w_next,
-                         const int32_t* __restrict__ cache_slot, int n_slots, int n_heads, int n_groups,
-                         int* d_status) {
+                         const int32_t* __restrict__ cache_slot, int n_slots, int n_heads, int* d_status) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = align_smem_1024(smem_raw);
+  constexpr int kRing = f8_ring(kPair), kRingPer = f8_ring_per(kPair), kStages8 = f8_stages(kPair), kOwn = f8_own(kPair);
+  constexpr int kCols = kPair ? kH : kF8Heads;  // heads of O and P
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int unit = blockIdx.x / n_groups;
-  const int h0 = (blockIdx.x % n_groups) * kF8Heads;  // the groups of a row run side by side and share its rows in L2
+  const uint32_t rank = kPair ? cluster_ctarank() : 0u, peer = rank ^ 1u;
+  const int unit = kPair ? blockIdx.x >> 1 : blockIdx.x;
   const int b = unit / n_split, split = unit % n_split;
   const int k_begin = split * span, k_end = min(K, k_begin + span);
   const int n_tiles = (k_end - k_begin + kF8Nt - 1) / kF8Nt;
+  const int h0 = (int)rank * kF8Heads;
   const int live = min(kF8Heads, n_heads - h0);
+  // the CTA's own latent columns are 128 (kOwn rank + i).., the peer's follow them
+  auto lat = [&](int i) -> int { return ((int)(kOwn * rank) + i) & 3; };
   int ep = end_pos[b];
   ep = ep < 0 ? 0 : (ep > S_max ? S_max : ep);
   int slot = b;
@@ -194,395 +229,562 @@ sparse_attend_fp8_kernel(const __nv_bfloat16* __restrict__ q_lat, const __nv_bfl
   }
 
   const uint32_t s0 = smem_u32(smem);
-  float* sc = reinterpret_cast<float*>(smem + kF8OffScale);
-  float* red = reinterpret_cast<float*>(smem + kF8OffRed);
-  float* mref = reinterpret_cast<float*>(smem + kF8OffRef);
-  float* alpha = reinterpret_cast<float*>(smem + kF8OffAlpha);
+  float* key = reinterpret_cast<float*>(smem + kF8OffKey);      // [tile & 3][s | log2 s | 1/s][128]
+  float* red = reinterpret_cast<float*>(smem + kF8OffRed);      // [tile & 1][position half][head]
+  int* pos_s = reinterpret_cast<int*>(smem + kF8OffPos);        // [tile & 3][128]
+  F8Move* moves = reinterpret_cast<F8Move*>(smem + kF8OffMove);  // [tile & 1][rank]
+  float* fin = reinterpret_cast<float*>(smem + kF8OffFin);
   F8Bars* bars = reinterpret_cast<F8Bars*>(smem + kF8OffBar);
   const AbortState ab{&bars->abort_flag, d_status};
 
   if (tid == 0) {
     bars->abort_flag = 0;
+    mbar_init(smem_u32(&bars->q_tma), 1);
     mbar_init(smem_u32(&bars->q_full), kF8SoftmaxWarps);
-    for (int s = 0; s < 2; ++s) {
-      for (int i = 0; i < 5; ++i) mbar_init(smem_u32(&bars->full[s][i]), kF8Nt);
-      for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&bars->empty[s][i]), 1);
-      mbar_init(smem_u32(&bars->pe_done[s]), 1);
-      mbar_init(smem_u32(&bars->sc_full[s]), kF8GatherWarps);
-      mbar_init(smem_u32(&bars->s_full[s]), 1);
-      mbar_init(smem_u32(&bars->s_empty[s]), kF8SoftmaxWarps);
+    for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&bars->ring_full[i]), 32 * kF8GatherWarps * kRingPer);
+    for (int i = 0; i < kRing; ++i) mbar_init(smem_u32(&bars->ring_empty[i]), 1);
+    for (int s = 0; s < kStages8; ++s) {
+      mbar_init(smem_u32(&bars->own_full[s]), 32 * kF8GatherWarps * kOwn);
+      mbar_init(smem_u32(&bars->own_empty[s]), 1);
     }
-    mbar_init(smem_u32(&bars->p_full), kF8SoftmaxWarps);
-    mbar_init(smem_u32(&bars->p_free), 1);
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(smem_u32(&bars->tile_full[s]), 1);
+      mbar_init(smem_u32(&bars->tile_done[s]), 1);
+    }
+    mbar_init(smem_u32(&bars->s_full), 1);
+    mbar_init(smem_u32(&bars->s_empty), kF8SoftmaxWarps);
+    mbar_init(smem_u32(&bars->p_own), kF8SoftmaxWarps);
+    mbar_init(smem_u32(&bars->p_hi), 1);
+    mbar_init(smem_u32(&bars->p_lo), 1);
+    for (int s = 0; s < 2; ++s) mbar_init(smem_u32(&bars->moves[s]), 1);
+    if (kPair) {  // armed for the first tiles
+      mbar_arrive_expect_tx(smem_u32(&bars->p_hi), kF8Limb);
+      mbar_arrive_expect_tx(smem_u32(&bars->p_lo), kF8Limb);
+      for (int s = 0; s < 2; ++s) mbar_arrive_expect_tx(smem_u32(&bars->moves[s]), sizeof(F8Move));
+    }
+    mbar_init(smem_u32(&bars->p_free), kPair ? 2 : 1);
     fence_mbarrier_init_cluster();
   }
   if (warp == kF8PvWarp) {
     tmem_alloc(smem_u32(&bars->tmem_addr), 512);
     tmem_relinquish();
   }
-  if (tid < kF8Heads) mref[tid] = kF8NoRef;
+  if (tid < kH) fin[tid] = 0.f;
   tc_fence_before();
-  __syncthreads();
+  if (kPair)
+    cluster_sync();  // barriers of both CTAs initialised before any remote access
+  else
+    __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_addr;
   grid_dep_launch();  // the value-up kernel may start loading its weights
 
-  if (warp >= kF8GatherWarp) {
-    // ------------------------------------------------------------ gather
-    // Lane l of warp g owns position 32 g + l of every tile: its index, its
-    // scale, its L2 prefetch.  A copy instruction brings 128 bytes of four
-    // positions.  Nothing here waits for a copy: the barriers complete when
-    // the data lands.
-    const int g = warp - kF8GatherWarp;
-    const int32_t* idx_row = topk_idx + (size_t)b * K;
-    const uint8_t* kv_row = kv8 + (size_t)slot * S_max * kDl;
-    const uint8_t* pe_row = reinterpret_cast<const uint8_t*>(pe8 + (size_t)slot * S_max * kDr);
+  const int qd = warp & 3, ch = warp >> 2;  // softmax warps
+  constexpr uint32_t kSoftmaxThreads = 32 * kF8SoftmaxWarps;
+
+  const int32_t* idx_row = topk_idx + (size_t)b * K;
+  const uint8_t* kv_row = kv8 + (size_t)slot * S_max * kDl;
+  const uint8_t* pe_row = reinterpret_cast<const uint8_t*>(pe8 + (size_t)slot * S_max * kDr);
+
+  if (warp == kF8IndexWarp) {
+    // ------------------------------------------------------------ positions
+    // Up to four tiles ahead of PV: the tile's positions, what their scales
+    // enter by (a masked position weighs exactly 0), and the L2 prefetch of the
+    // next tile's rows (a pair's CTAs take half of them each).  The loads for
+    // the tiles after that are in flight meanwhile.
     const float* sc_row = kv_scale + (size_t)slot * n_blocks;
-    auto load_idx = [&](int j) -> int {
-      const int k = k_begin + j * kF8Nt + 32 * g + lane;
-      const int v = k < k_end ? __ldg(idx_row + k) : -1;
-      return (v >= 0 && v < ep) ? v : -1;
+    struct Four {
+      int pos[4];
     };
-    auto load_scale = [&](int pos) -> float { return pos >= 0 ? __ldg(sc_row + (pos >> block_shift)) : 0.f; };
-    auto prefetch = [&](int pos) {
-      if (pos >= 0) {
-        const uint8_t* r = kv_row + (size_t)pos * kDl;
+    auto load = [&](int j) -> Four {  // positions 32 i + lane of tile j
+      Four f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) asm volatile("prefetch.global.L2 [%0];" ::"l"(r + i * 128));
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(pe_row + (size_t)pos * (kDr * 2)));
+      for (int i = 0; i < 4; ++i) {
+        const int k = k_begin + j * kF8Nt + 32 * i + lane;
+        const int v = k < k_end ? __ldg(idx_row + k) : -1;
+        f.pos[i] = (v >= 0 && v < ep) ? v : -1;
+      }
+      return f;
+    };
+    auto prefetch = [&](const Four& f) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (f.pos[i] < 0 || (kPair && (i >> 1) != (int)rank)) continue;
+        const uint8_t* r = kv_row + (size_t)f.pos[i] * kDl;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) asm volatile("prefetch.global.L2 [%0];" ::"l"(r + u * 128));
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(pe_row + (size_t)f.pos[i] * (kDr * 2)));
       }
     };
-    auto copy = [&](uint32_t dst, const uint8_t* base, int row_bytes, int idx) {
+    Four cur = load(0), next = load(1);
+    float sv[4], sv_next[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = 4 * i + (lane >> 3);
-        const int pos = __shfl_sync(0xffffffffu, idx, r);
-        const size_t p = pos >= 0 ? (size_t)pos : 0;
-        cp_async_16(dst + sw128_offset(32 * g + r, lane & 7), base + p * row_bytes + (lane & 7) * 16,
-                    pos >= 0 ? 16u : 0u);
-      }
-    };
-    int idx0 = load_idx(0), idx1 = load_idx(1);
-    float sc0 = load_scale(idx0);
-    prefetch(idx1);
+    for (int i = 0; i < 4; ++i) sv[i] = cur.pos[i] >= 0 ? __ldg(sc_row + (cur.pos[i] >> block_shift)) : 0.f;
     for (int j = 0; j < n_tiles; ++j) {
-      const int st = j & 1;
-      const uint32_t ph = (j >> 1) & 1, was = ph ^ 1;
-      const uint32_t stage = s0 + st * kF8StageBytes;
-      const int idx2 = load_idx(j + 2);
-      const float sc1 = load_scale(idx1);
-      if (j >= 2) wait(smem_u32(&bars->empty[st][0]), was, ab);
-      copy(stage, pe_row, kDr * 2, idx0);
-      cp_async_arrive(smem_u32(&bars->full[st][4]));
-      sc[st * kF8Nt + 32 * g + lane] = sc0;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars->sc_full[st]));
+      const Four next2 = load(j + 2);
 #pragma unroll
-      for (int i = 1; i < 4; ++i) {
-        if (j >= 2) wait(smem_u32(&bars->empty[st][i]), was, ab);
-        copy(stage + i * kF8Block, kv_row + i * 128, kDl, idx0);
-        cp_async_arrive(smem_u32(&bars->full[st][i]));
+      for (int i = 0; i < 4; ++i) sv_next[i] = next.pos[i] >= 0 ? __ldg(sc_row + (next.pos[i] >> block_shift)) : 0.f;
+      if (j >= 4) wait(smem_u32(&bars->tile_done[j & 3]), ((j >> 2) - 1) & 1, ab);
+      float* kt = key + (j & 3) * (3 * kF8Nt);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int n = 32 * i + lane;
+        const bool on = !(sv[i] <= 0.f);
+        pos_s[(j & 3) * kF8Nt + n] = cur.pos[i];
+        kt[n] = sv[i];
+        kt[kF8Nt + n] = on ? __log2f(sv[i]) : -INFINITY;
+        kt[2 * kF8Nt + n] = on ? __frcp_rn(sv[i]) : 0.f;
       }
-      prefetch(idx2);
-      wait(smem_u32(&bars->pe_done[st]), ph, ab);
-      copy(stage, kv_row, kDl, idx0);
-      cp_async_arrive(smem_u32(&bars->full[st][0]));
-      idx0 = idx1;
-      idx1 = idx2;
-      sc0 = sc1;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars->tile_full[j & 3]));
+      prefetch(next);
+      cur = next;
+      next = next2;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sv[i] = sv_next[i];
     }
     // One head's W_UV into L2 for the value-up kernel that follows.
-    if (g == 0 && lane == 0 && w_next != nullptr && (int)blockIdx.x < n_heads) {
+    if (lane == 0 && w_next != nullptr && (int)blockIdx.x < n_heads) {
       const __nv_bfloat16* w = w_next + (size_t)(blockIdx.x * kHeadRows + kDn) * kDl;
 #pragma unroll
       for (int part = 0; part < 4; ++part) prefetch_l2(w + part * 32 * kDl, 32 * kDl * 2);
     }
+  } else if (warp >= kF8GatherWarp && warp < kF8GatherWarp + kF8GatherWarps) {
+    // ------------------------------------------------------------ gather
+    // A copy instruction brings 128 bytes of four positions; the warps
+    // share a block's 32 of them, each with its positions in registers for all
+    // five blocks (read for each copy, the copies issued at half the rate).
+    // Nothing here waits for a copy: the barriers complete when the data
+    // lands.
+    const int g = warp - kF8GatherWarp;
+    constexpr int kCopies = 32 / kF8GatherWarps;
+    int rs = 0, st = 0;          // ring slot, stage
+    uint32_t rph = 1, sph = 1;   // parity of the release to wait for (passes at once the first time round)
+    const uint32_t dst0 = s0 + sw128_offset(4 * g + (lane >> 3), lane & 7);
+    for (int j = 0; j < n_tiles; ++j) {
+      int pos[kCopies];
+      wait(smem_u32(&bars->tile_full[j & 3]), (j >> 2) & 1, ab);
+#pragma unroll
+      for (int i = 0; i < kCopies; ++i) pos[i] = pos_s[(j & 3) * kF8Nt + 4 * (g + kF8GatherWarps * i) + (lane >> 3)];
+      // the rotary rows, then 128 columns at a time: the peer's, the CTA's own
+      // (one body for all: the warps of an SM fetch more code than its
+      // instruction cache likes)
+#pragma unroll 1
+      for (int i = 0; i < 5; ++i) {
+        const bool ring = i < kRingPer;
+        uint64_t* full;
+        uint32_t dst;
+        if (ring) {
+          wait(smem_u32(&bars->ring_empty[rs]), rph, ab);
+          full = &bars->ring_full[j & 1];
+          dst = dst0 + rs * kF8Block;
+          if (++rs == kRing) rs = 0, rph ^= 1;
+        } else {
+          if (i == kRingPer) {
+            // the query's boxes lie in the stages behind the first until they are in TMEM
+            if (j == 1) wait(smem_u32(&bars->q_full), 0, ab);
+            wait(smem_u32(&bars->own_empty[st]), sph, ab);
+          }
+          full = &bars->own_full[st];
+          dst = dst0 + f8_own_at(kPair, 0, 0) + (st * kOwn + i - kRingPer) * kF8Block;
+        }
+        const uint8_t* src = (i == 0 ? pe_row : kv_row + lat(ring ? kOwn + i - 1 : i - kRingPer) * 128) + (lane & 7) * 16;
+        const uint32_t row_bytes = i == 0 ? kDr * 2 : kDl;
+#pragma unroll
+        for (int u = 0; u < kCopies; ++u) {
+          cp_async_16(dst + u * (4 * kF8GatherWarps * 128), src + (uint64_t)max(pos[u], 0) * row_bytes, pos[u] >= 0 ? 16u : 0u);
+        }
+        cp_async_arrive(smem_u32(full));
+      }
+      if (++st == kStages8) st = 0, sph ^= 1;
+    }
   } else if (warp == kF8QkWarp) {
-    // ------------------------------------------------------------ QK issue
+    // ------------------------------------------------ query load, QK issue
     if (lane == 0) {
-      constexpr uint32_t id_pe = idesc_bf16_f32(128, 64, false, false);
-      constexpr uint32_t id_half = idesc_e4m3_f32(128, 64, false, false);
-      constexpr uint32_t id_both = idesc_e4m3_f32(128, 128, false, false);
-      const uint64_t d_stage = smem_desc_sw128(s0, 16, 1024);
-      const uint64_t d_q = smem_desc_sw128(s0 + kF8OffQ, 16, 1024);
+      // eight boxes of 64 columns x 64 heads (heads past the call's read as zero)
+      tma_prefetch_desc(&tm_q);
+      grid_dep_wait();  // q_lat comes from the absorption kernel
+      mbar_arrive_expect_tx(smem_u32(&bars->q_tma), kF8Heads * kDl * 2);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        tma_load_3d(s0 + f8_own_at(kPair, 1, 0) + i * (kF8Heads * 128), &tm_q, smem_u32(&bars->q_tma), i * 64, h0, b);
+
+      constexpr uint32_t id_pe = idesc_bf16_f32(128, kF8Nt, false, false);
+      constexpr uint32_t id_qk = idesc_e4m3_f32(128, kF8Nt, false, false);
+      const uint64_t d_0 = smem_desc_sw128(s0, 16, 1024);
       const uint64_t d_qpe = smem_desc_sw128(s0 + kF8OffQpe, 16, 1024);
+      const uint32_t dst = tmem + kF8ColS, q = tmem + kF8ColQ;
+      auto qk = [&](uint64_t k0, int block) {  // 128 columns of the latent
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mma_f8_ts(dst, q + block * 32 + k * 8, k0 + (uint64_t)(k * 2), id_qk, 1u);
+      };
       wait(smem_u32(&bars->q_full), 0, ab);
+      int rs = 0, st = 0;
+      uint32_t sph = 0;
       for (int j = 0; j < n_tiles; ++j) {
-        const int st = j & 1;
-        const uint32_t ph = (j >> 1) & 1;
-        const uint64_t a0 = d_stage + (uint64_t)((st * kF8StageBytes) >> 4);
-        const uint32_t dst = tmem + kF8ColS + st * 128;
-        if (j >= 2) wait(smem_u32(&bars->s_empty[st]), ph ^ 1, ab);
-        wait(smem_u32(&bars->full[st][4]), ph, ab);
+        // One wait and one proxy fence for the ring blocks and one for the
+        // stage: a pair of them costs as much as a block's four MMAs.
+        wait(smem_u32(&bars->ring_full[j & 1]), (j >> 1) & 1, ab);
+        fence_proxy_async_smem();
+        if (j >= 1) wait(smem_u32(&bars->s_empty), (j - 1) & 1, ab);
+        tc_fence_after();
+#pragma unroll 1
+        for (int i = 0; i < kRingPer; ++i) {
+          const uint64_t k0 = d_0 + (uint64_t)((rs * kF8Block) >> 4);
+          if (i == 0) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma_ss(dst, d_qpe + (uint64_t)(k * 2), k0 + (uint64_t)(k * 2), id_pe, k > 0 ? 1u : 0u);
+          } else {
+            qk(k0, lat(kOwn + i - 1));
+          }
+          mma_commit(smem_u32(&bars->ring_empty[rs]));
+          if (++rs == kRing) rs = 0;
+        }
+        wait(smem_u32(&bars->own_full[st]), sph, ab);
         fence_proxy_async_smem();
         tc_fence_after();
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_ss(dst, a0 + (uint64_t)(k * 2), d_qpe + (uint64_t)(k * 2), id_pe, k > 0 ? 1u : 0u);
-        mma_commit(smem_u32(&bars->pe_done[st]));
-#pragma unroll
-        for (int o = 1; o <= 4; ++o) {
-          const int i = o & 3;  // blocks 1, 2, 3, 0
-          wait(smem_u32(&bars->full[st][i]), ph, ab);
-          fence_proxy_async_smem();
-          tc_fence_after();
-          const uint64_t a = a0 + (uint64_t)((i * kF8Block) >> 4);
-          const uint64_t q = d_q + (uint64_t)((i * kF8Block) >> 4);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (o == 1 && k == 0) {  // the hi columns hold the rotary product, the lo columns start at zero
-              mma_f8_ss(dst, a, q, id_half, 1u);
-              mma_f8_ss(dst + 64, a, q + (uint64_t)((kF8Heads * 128) >> 4), id_half, 0u);
-            } else {
-              mma_f8_ss(dst, a + (uint64_t)(k * 2), q + (uint64_t)(k * 2), id_both, 1u);
-            }
-          }
-        }
-        mma_commit(smem_u32(&bars->s_full[st]));
+#pragma unroll 1
+        for (int i = 0; i < kOwn; ++i)
+          qk(d_0 + (uint64_t)((f8_own_at(kPair, 0, 0) + (st * kOwn + i) * kF8Block) >> 4), lat(i));
+        if (++st == kStages8) st = 0, sph ^= 1;
+        mma_commit(smem_u32(&bars->s_full));
       }
     }
     __syncwarp();
   } else if (warp == kF8PvWarp) {
-    // ------------------------------------------------------------ PV issue
+    // ------------------------------------------------ pushes, PV issue
     if (lane == 0) {
-      constexpr uint32_t id_pv = idesc_e4m3_f32(128, 64, true, true);
-      const uint64_t d_stage = smem_desc_sw128(s0, 16, 1024);
-      const uint64_t d_p = smem_desc_sw64(s0 + kF8OffP, 512);
+      constexpr uint32_t id_pv = idesc_e4m3_f32(128, kCols, true, false);
+      const uint64_t d_0 = smem_desc_sw128(s0, 16, 1024);
+      const uint64_t p0 = d_0 + (uint64_t)(kF8OffP >> 4);
+      constexpr uint32_t kLoAt = (kPair ? 2 : 1) * kF8Limb;
+      const uint32_t src = s0 + kF8OffP + rank * kF8Limb, far = cluster_map(src, peer);
+      const uint32_t b_hi = cluster_map(smem_u32(&bars->p_hi), peer), b_lo = cluster_map(smem_u32(&bars->p_lo), peer);
+      int st = 0;
       for (int j = 0; j < n_tiles; ++j) {
-        const int st = j & 1;
-        wait(smem_u32(&bars->p_full), j & 1, ab);
-        tc_fence_after();
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          const uint64_t a = d_stage + (uint64_t)((st * kF8StageBytes + m * kF8Block) >> 4);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {  // 32 positions a step
-            const uint64_t ak = a + (uint64_t)((k * 32 * 128) >> 4);
-            const uint64_t pk = d_p + (uint64_t)((k * 32 * 64) >> 4);
-            mma_f8_ss(tmem + kF8ColO + m * 64, ak, pk, id_pv, (j > 0 || k > 0) ? 1u : 0u);
-            mma_f8_ss(tmem + kF8ColO + m * 64, ak, pk + (uint64_t)(kF8PBytes >> 4), id_pv, 1u);
-          }
-          mma_commit(smem_u32(&bars->empty[st][m]));
+        const uint32_t ph = j & 1;
+        wait(smem_u32(&bars->p_own), ph, ab);
+        if (kPair) {
+          // The peer's P is free: p_free(j - 1), which the softmax warps
+          // waited for, counts its PV too.
+          bulk_push(far, src, kF8Limb, b_hi);
+          bulk_push(far + kLoAt, src + kLoAt, kF8Limb, b_lo);
+          wait_cluster(smem_u32(&bars->p_hi), ph, ab);
+          if (j + 1 < n_tiles) mbar_arrive_expect_tx(smem_u32(&bars->p_hi), kF8Limb);
         }
-        mma_commit(smem_u32(&bars->p_free));
+        tc_fence_after();
+        // 128 latent columns x the heads, 32 positions a step, hi limbs and
+        // lo limbs.  Pair: all hi limbs first, the peer's lo limbs are still
+        // on their way.
+        const uint64_t v0 = d_0 + (uint64_t)((f8_own_at(kPair, 0, 0) + st * (kOwn * kF8Block)) >> 4);
+        auto pv = [&](int m, int k, int lo, bool first) {
+          mma_f8_ss(tmem + kF8ColO + m * kCols, v0 + (uint64_t)((m * kF8Block + k * 32 * 128) >> 4),
+                    p0 + (uint64_t)((lo * kLoAt + k * 32) >> 4), id_pv, first ? 0u : 1u);
+        };
+        if (kPair) {
+#pragma unroll 1
+          for (int m = 0; m < kOwn; ++m)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) pv(m, k, 0, j == 0 && k == 0);
+          wait_cluster(smem_u32(&bars->p_lo), ph, ab);
+          if (j + 1 < n_tiles) mbar_arrive_expect_tx(smem_u32(&bars->p_lo), kF8Limb);
+        }
+#pragma unroll 1
+        for (int m = 0; m < kOwn; ++m)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (!kPair) pv(m, k, 0, j == 0 && k == 0);
+            pv(m, k, 1, false);
+          }
+        mma_commit(smem_u32(&bars->own_empty[st]));
+        mma_commit(smem_u32(&bars->tile_done[j & 3]));
+        if (kPair)
+          mma_commit_to(smem_u32(&bars->p_free), (uint16_t)3);
+        else
+          mma_commit(smem_u32(&bars->p_free));
+        if (++st == kStages8) st = 0;
       }
     }
     __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax
-    const int qd = warp & 3, hh = warp >> 2;
-    const int row = 32 * qd + lane;  // position of the tile
+    const int hd = 16 * qd + (lane & 15);  // head; lanes 0..15 hold its hi row, 16..31 its lo row
+    const bool hi_row = lane < 16;
     const uint32_t lane_base = (uint32_t)(qd * 32) << 16;
-    constexpr uint32_t kAll = 32 * kF8SoftmaxWarps;
-    auto fmax2 = [](float x, float y) { return fmaxf(x, y); };
-    auto fadd2 = [](float x, float y) { return x + y; };
 
     // The query's limbs.  One power of two for the CTA's 64 heads: a softmax
     // feels the absolute error of a score, and a head of small queries gets
-    // the same absolute error as the largest one.
+    // the same absolute error as the largest one.  A thread takes 256 columns
+    // of its row (both rows of a head read the same values).
     float c2;  // scores to log2 units
+    bool bad;
     {
-      grid_dep_wait();  // q_lat comes from the absorption kernel
-      const uint4* src = reinterpret_cast<const uint4*>(q_lat + ((size_t)b * n_heads + h0) * kDl);
-      uint4 v[16];
-      float am = 0.f;
+      const uint32_t box = s0 + f8_own_at(kPair, 1, 0) + (uint32_t)(4 * ch) * (kF8Heads * 128) + (uint32_t)hd * 128u;
+      auto piece = [&](int c) {  // eight of the 256 columns
+        return ld_shared_v4(box + (uint32_t)(c >> 3) * (kF8Heads * 128) + (uint32_t)(((c & 7) ^ (hd & 7)) << 4));
+      };
+      // the rotary part's row, from memory
+      uint4 r4[4];
+      const uint4* psrc = reinterpret_cast<const uint4*>(q_pe + ((size_t)b * n_heads + h0 + hd) * kDr) + 4 * ch;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int c = i * (int)kAll + tid;  // 16-byte piece c of the 64 x 64
-        v[i] = (c >> 6) < live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-        am = fmaxf(am, amax8(v[i]));
+      for (int u = 0; u < 4; ++u) r4[u] = hi_row && hd < live ? __ldg(psrc + u) : make_uint4(0, 0, 0, 0);
+
+      wait(smem_u32(&bars->q_tma), 0, ab);
+      uint32_t m2 = 0;
+#pragma unroll 8
+      for (int c = 0; c < 16; ++c) {  // the two rows of a head share its columns
+        const uint4 v = piece(2 * c + (hi_row ? 0 : 1));
+        m2 = amax2(amax2(amax2(amax2(m2, v.x), v.y), v.z), v.w);
       }
+      uint32_t m = max(m2 & 0xffffu, m2 >> 16);
+      if (m >= 0x7f80u) {  // an infinity or NaN: the head's scores are NaN, the others' scale is not its
+        fin[hd] = 1.f;
+        m = 0;
+      }
+      m = __reduce_max_sync(0xffffffffu, m);
+      if (lane == 0) red[warp] = __uint_as_float(m << 16);
+      named_bar_sync(1, kSoftmaxThreads);
+      bad = fin[hd] != 0.f;
+      float am = red[0];
 #pragma unroll
-      for (int s = 16; s >= 1; s >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, s));
-      if (lane == 0) red[warp] = am;
-      named_bar_sync(1, kAll);
-#pragma unroll
-      for (int w = 0; w < kF8SoftmaxWarps; ++w) am = fmaxf(am, red[w]);
+      for (int w = 1; w < kF8SoftmaxWarps; ++w) am = fmaxf(am, red[w]);
       const int e = limb_exponent(am);
       const float mul = exp2_int(e);
       c2 = scale * 1.4426950408889634f * exp2_int(-e);
+#pragma unroll 2
+      for (int c = 0; c < 16; ++c) {  // 16 columns: of two pieces, each row of the head converts one
+        const uint4 v = piece(2 * c + (hi_row ? 0 : 1));
+        uint32_t r[4];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int c = i * (int)kAll + tid, hd = c >> 6, piece = c & 63;
-        uint2 hi, lo;
-        limbs8(v[i], mul, &hi, &lo);
-        const uint32_t dst = s0 + kF8OffQ + (piece >> 4) * kF8Block + sw128_offset(hd, (piece & 15) >> 1) + (piece & 1) * 8;
-        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst), "r"(hi.x), "r"(hi.y) : "memory");
-        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst + kF8Heads * 128), "r"(lo.x), "r"(lo.y) : "memory");
+        for (int u = 0; u < 2; ++u) {
+          uint32_t hi, lo;
+          limbs4(u ? v.z : v.x, u ? v.w : v.y, mul * (1.f / 256.f), &hi, &lo);
+          const uint32_t other = __shfl_xor_sync(0xffffffffu, hi_row ? lo : hi, 16);
+          r[u] = hi_row ? hi : other;
+          r[2 + u] = hi_row ? other : lo;
+        }
+        tmem_st4(tmem + lane_base + kF8ColQ + 64 * ch + 4 * c, r);
       }
-      const uint4* psrc = reinterpret_cast<const uint4*>(q_pe + ((size_t)b * n_heads + h0) * kDr);
+      tmem_wait_st();
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int c = i * (int)kAll + tid, hd = c >> 3;
-        const uint4 r = hd < live ? __ldg(psrc + c) : make_uint4(0, 0, 0, 0);
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+      for (int u = 0; u < 4; ++u) {
+        const uint32_t w[4] = {r4[u].x, r4[u].y, r4[u].z, r4[u].w};
         uint32_t o[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u)  // times a power of two: exact
-          o[u] = pack_bf16x2(__uint_as_float(w[u] << 16) * mul, __uint_as_float(w[u] & 0xffff0000u) * mul);
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(s0 + kF8OffQpe + sw128_offset(hd, c & 7)),
-                     "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
-                     : "memory");
+        for (int i = 0; i < 4; ++i)  // times a power of two: exact
+          o[i] = pack_bf16x2(__uint_as_float(w[i] << 16) * mul, __uint_as_float(w[i] & 0xffff0000u) * mul);
+        st_shared_v4(s0 + kF8OffQpe + sw128_offset(32 * qd + lane, 4 * ch + u), o[0], o[1], o[2], o[3]);
       }
       fence_proxy_async_smem();
+      tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars->q_full));
     }
 
-    const float4* mref4 = reinterpret_cast<const float4*>(mref + 32 * hh);
-    const float4* alpha4 = reinterpret_cast<const float4*>(alpha + 32 * hh);
-    float l[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) l[i] = 0.f;
-
+    // Of the 64 positions of the warp, lanes 0..15 finish the first 32 and
+    // lanes 16..31 the others: each sends its partner the other half.
+    const int first = 64 * ch + (hi_row ? 0 : 32);
+    if (bad) c2 = __int_as_float(0x7fffffff);
+    const float w_k = hi_row ? c2 : c2 * kLimbLo, w_r = hi_row ? c2 * kLimbLo : c2;
+    const uint64_t w_keep = pack_f32x2(w_k, w_k), w_recv = pack_f32x2(w_r, w_r);
+    float m_ref = kF8NoRef, l = 0.f;
     for (int j = 0; j < n_tiles; ++j) {
-      const int st = j & 1;
-      const uint32_t ph = (j >> 1) & 1;
-      wait(smem_u32(&bars->sc_full[st]), ph, ab);
-      const float s_t = sc[st * kF8Nt + row];
-      const bool on = s_t > 0.f;
-      const float f = s_t * c2;
-      const float lg = on ? __log2f(s_t) : -INFINITY;
-      const float rs = on ? __frcp_rn(s_t) : 0.f;
-      wait(smem_u32(&bars->s_full[st]), ph, ab);
+      const ulonglong2* kt = reinterpret_cast<const ulonglong2*>(key + (j & 3) * (3 * kF8Nt) + first);
+      F8Move* mv = moves + 2 * (j & 1) + rank;  // tile j - 2's is done: P(j - 1) came after its PVs
+      uint64_t y[16];  // pairs of positions
+      wait(smem_u32(&bars->s_full), j & 1, ab);
       tc_fence_after();
-      float y[32];
       {
-        uint32_t hi[32], lo[32];
-        tmem_ld32(tmem + lane_base + kF8ColS + st * 128 + 32 * hh, hi);
-        tmem_ld32(tmem + lane_base + kF8ColS + st * 128 + 64 + 32 * hh, lo);
+        uint32_t v[64];
+        tmem_ld32(tmem + lane_base + kF8ColS + 64 * ch, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
+        tmem_ld32(tmem + lane_base + kF8ColS + 64 * ch + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
         tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->s_empty));
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          y[i] = fmaf(fmaf(__uint_as_float(lo[i]), kLimbLo, __uint_as_float(hi[i])), f, lg);
+        for (int i = 0; i < 16; ++i) {
+          float keep[2], recv[2];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const uint32_t a = v[2 * i + u], c = v[32 + 2 * i + u];
+            keep[u] = __uint_as_float(hi_row ? a : c);
+            recv[u] = __shfl_xor_sync(0xffffffffu, __uint_as_float(hi_row ? c : a), 16);
+          }
+          y[i] = fma_f32x2(pack_f32x2(keep[0], keep[1]), w_keep, mul_f32x2(pack_f32x2(recv[0], recv[1]), w_recv));
+        }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars->s_empty[st]));
-
-      float top = -INFINITY;
+      wait(smem_u32(&bars->tile_full[j & 3]), (j >> 2) & 1, ab);
+      float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
-        const float4 m = mref4[q];
-        top = fmaxf(top, fmaxf(fmaxf(y[4 * q] - m.x, y[4 * q + 1] - m.y), fmaxf(y[4 * q + 2] - m.z, y[4 * q + 3] - m.w)));
+        const ulonglong2 f = kt[q], g = kt[kF8Nt / 4 + q];
+        y[2 * q] = fma_f32x2(y[2 * q], f.x, g.x);
+        y[2 * q + 1] = fma_f32x2(y[2 * q + 1], f.y, g.y);
+        const float2 a = unpack_f32x2(y[2 * q]), c = unpack_f32x2(y[2 * q + 1]);
+        top4[q & 3] = fmaxf(fmaxf(top4[q & 3], fmaxf(a.x, a.y)), fmaxf(c.x, c.y));
       }
-      if (named_bar_or(1, kAll, top > kF8RefLimit)) {
-        // Some P leaves E4M3's range: the tile's largest y of every head, the
-        // new m_h of the heads it asks for, and O and the sums brought to it.
-        float t[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) t[i] = y[i];
-        red[qd * kF8Heads + 32 * hh + lane] = reduce_transposed(t, lane, fmax2);
-        named_bar_sync(1, kAll);
-        if (tid < kF8Heads) {
-          const float mx = fmaxf(fmaxf(red[tid], red[kF8Heads + tid]), fmaxf(red[2 * kF8Heads + tid], red[3 * kF8Heads + tid]));
-          const float old = mref[tid];
-          const float now = mx - old > kF8RefLimit ? mx + kF8RefMargin : old;
-          alpha[tid] = ex2_approx(old - now);
-          mref[tid] = now;
+      float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+      // the head's other 64 positions (two buffers: a warp may run a tile ahead)
+      float* rt = red + (j & 1) * (2 * kF8Heads);
+      if (hi_row) rt[ch * kF8Heads + hd] = top;
+      named_bar_sync(2 + qd, 64);
+      top = fmaxf(top, rt[(ch ^ 1) * kF8Heads + hd]);
+
+      const bool move = top - m_ref > kF8RefLimit;
+      const float now = move ? top + kF8RefMargin : m_ref;
+      const float factor = move ? ex2_approx(m_ref - now) : 1.f;
+      // nothing to rescale before the first PV
+      const uint32_t moved = j > 0 ? __ballot_sync(0xffffffffu, move) & 0xffffu : 0u;
+      if (ch == 0) {
+        const uint32_t far = cluster_map(smem_u32(&bars->moves[j & 1]), peer);
+        if (hi_row) {
+          mv->factor[hd] = factor;
+          if (kPair) st_async_b32(cluster_map(smem_u32(&mv->factor[hd]), peer), __float_as_uint(factor), far);
         }
-        named_bar_sync(1, kAll);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const float4 a = alpha4[q];
-          l[4 * q] *= a.x, l[4 * q + 1] *= a.y, l[4 * q + 2] *= a.z, l[4 * q + 3] *= a.w;
+        if (lane == 0) {
+          mv->moved[qd] = moved;
+          if (kPair) st_async_b32(cluster_map(smem_u32(&mv->moved[qd]), peer), moved, far);
         }
-        if (j > 0) {
-          wait(smem_u32(&bars->p_free), (j - 1) & 1, ab);  // every PV issued so far is done
+      }
+      m_ref = now;
+      l *= factor;
+
+      // P and its limbs, four positions a word.
+      uint32_t p_hi[8], p_lo[8];
+      uint64_t l2[2] = {0, 0};
+      const uint64_t minus_m = pack_f32x2(-m_ref, -m_ref);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const ulonglong2 r = kt[2 * (kF8Nt / 4) + q];
+        const float2 ya = unpack_f32x2(add_f32x2(y[2 * q], minus_m)), yc = unpack_f32x2(add_f32x2(y[2 * q + 1], minus_m));
+        const float p0 = ex2_approx(ya.x), p1 = ex2_approx(ya.y), p2 = ex2_approx(yc.x), p3 = ex2_approx(yc.y);
+        l2[0] = fma_f32x2(pack_f32x2(p0, p1), r.x, l2[0]);
+        l2[1] = fma_f32x2(pack_f32x2(p2, p3), r.y, l2[1]);
+        const uint32_t f01 = pack_f16x2_sat(p0, p1), f23 = pack_f16x2_sat(p2, p3);
+        const uint32_t a01 = limb_first(f01), a23 = limb_first(f23);
+        p_hi[q] = limb_bytes_positive(a01, a23);
+        p_lo[q] = limb_bytes(limb_first(half2_bits(limb_rest(f01, a01))), limb_first(half2_bits(limb_rest(f23, a23))));
+      }
+      const float2 l01 = unpack_f32x2(add_f32x2(l2[0], l2[1]));
+      l += l01.x + l01.y;
+
+      // The heads of either CTA that moved: their columns of this CTA's O,
+      // between PV(j - 1) and PV(j); 16 columns that hold none of them are left
+      // alone.  The CTA's own words come from its other warps.
+      if (kPair) {
+        wait_cluster(smem_u32(&bars->moves[j & 1]), (j >> 1) & 1, ab);
+        if (tid == 0 && j + 2 < n_tiles) mbar_arrive_expect_tx(smem_u32(&bars->moves[j & 1]), sizeof(F8Move));
+      }
+      named_bar_sync(1, kSoftmaxThreads);
+      if (j > 0) {
+        wait_cluster(smem_u32(&bars->p_free), (j - 1) & 1, ab);  // the one P buffer; O is stable
+        const F8Move* both = moves + 2 * (j & 1);
+        const uint4 w0 = *reinterpret_cast<const uint4*>(both[0].moved);
+        const uint4 w1 = kPair ? *reinterpret_cast<const uint4*>(both[1].moved) : make_uint4(0, 0, 0, 0);
+        if ((w0.x | w0.y | w0.z | w0.w | w1.x | w1.y | w1.z | w1.w) != 0) {
           tc_fence_after();
 #pragma unroll 1
           for (int cc = 0; cc < 8; ++cc) {
-            const uint32_t at = tmem + lane_base + kF8ColO + 128 * hh + cc * 16;
+            const int col = (cc * 16) % kCols, h16 = col % kF8Heads;
+            const F8Move* who = both + col / kF8Heads;
+            if (who->moved[h16 >> 4] == 0) continue;
+            const uint32_t at = tmem + lane_base + kF8ColO + 128 * ch + cc * 16;
             uint32_t ov[16];
             tmem_ld16(at, ov);
             tmem_wait_ld();
+            const float4* f4 = reinterpret_cast<const float4*>(who->factor + h16);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha[(cc & 3) * 16 + i]);
+            for (int i = 0; i < 4; ++i) {
+              const float4 f = f4[i];
+              ov[4 * i] = __float_as_uint(__uint_as_float(ov[4 * i]) * f.x);
+              ov[4 * i + 1] = __float_as_uint(__uint_as_float(ov[4 * i + 1]) * f.y);
+              ov[4 * i + 2] = __float_as_uint(__uint_as_float(ov[4 * i + 2]) * f.z);
+              ov[4 * i + 3] = __float_as_uint(__uint_as_float(ov[4 * i + 3]) * f.w);
+            }
             tmem_st16(at, ov);
           }
           tmem_wait_st();
+          tc_fence_before();
         }
       }
-
-      // P and its limbs, four heads a word: the hi limb is the fp16 number
-      // truncated to E4M3's bits, the lo limb what that left, rounded.
-      uint32_t ph4[8], pl4[8];
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const float4 m = mref4[q];
-        const float p0 = ex2_approx(y[4 * q] - m.x), p1 = ex2_approx(y[4 * q + 1] - m.y);
-        const float p2 = ex2_approx(y[4 * q + 2] - m.z), p3 = ex2_approx(y[4 * q + 3] - m.w);
-        l[4 * q] = fmaf(p0, rs, l[4 * q]);
-        l[4 * q + 1] = fmaf(p1, rs, l[4 * q + 1]);
-        l[4 * q + 2] = fmaf(p2, rs, l[4 * q + 2]);
-        l[4 * q + 3] = fmaf(p3, rs, l[4 * q + 3]);
-        uint32_t h[2], r[2];
-        h[0] = pack_f16x2_sat(p0, p1);
-        h[1] = pack_f16x2_sat(p2, p3);
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const uint32_t cut = h[u] & 0x3f803f80u;
-          __half2 a, c;
-          memcpy(&a, &h[u], 4);
-          memcpy(&c, &cut, 4);
-          const __half2 d = __hsub2(a, c);
-          memcpy(&r[u], &d, 4);
-          r[u] += 0x00400040u;
-        }
-        ph4[q] = __byte_perm(h[0] << 1, h[1] << 1, 0x7531);
-        pl4[q] = __byte_perm(r[0] << 1, r[1] << 1, 0x7531);
-      }
-      if (j > 0) wait(smem_u32(&bars->p_free), (j - 1) & 1, ab);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const uint32_t dst = s0 + kF8OffP + sw64_offset(row, 2 * hh + u);
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(ph4[4 * u]), "r"(ph4[4 * u + 1]),
-                     "r"(ph4[4 * u + 2]), "r"(ph4[4 * u + 3])
-                     : "memory");
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + kF8PBytes), "r"(pl4[4 * u]),
-                     "r"(pl4[4 * u + 1]), "r"(pl4[4 * u + 2]), "r"(pl4[4 * u + 3])
-                     : "memory");
+        const uint32_t dst = s0 + kF8OffP + rank * kF8Limb + sw128_offset(hd, (first >> 4) + u);
+        st_shared_v4(dst, p_hi[4 * u], p_hi[4 * u + 1], p_hi[4 * u + 2], p_hi[4 * u + 3]);
+        st_shared_v4(dst + (kPair ? 2 : 1) * kF8Limb, p_lo[4 * u], p_lo[4 * u + 1], p_lo[4 * u + 2], p_lo[4 * u + 3]);
       }
       fence_proxy_async_smem();
-      tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars->p_full));
+      if (lane == 0) mbar_arrive(smem_u32(&bars->p_own));
     }
 
-    // Epilogue: the row sums over the positions, O normalised and turned
-    // round through the idle stages (a head's 512 columns contiguous), one
-    // bulk copy a head.
-    red[qd * kF8Heads + 32 * hh + lane] = reduce_transposed(l, lane, fadd2);
-    named_bar_sync(1, kAll);
-    if (tid < kF8Heads) {
-      const float sum = (red[tid] + red[kF8Heads + tid]) + (red[2 * kF8Heads + tid] + red[3 * kF8Heads + tid]);
-      alpha[tid] = sum == 0.f ? 0.f : (1.f / 256.f) / sum;  // P's E4M3 value is 2^8 times its fp16 one
-      if (tid < live)
-        lse_part[((size_t)b * n_split + split) * n_heads + h0 + tid] =
-            sum == 0.f ? -INFINITY : (mref[tid] + log2f(sum)) * 0.6931471805599453f;
+    // The row sums over the positions; what normalises O goes to the peer too.
+    l += __shfl_xor_sync(0xffffffffu, l, 16);
+    named_bar_sync(2 + qd, 64);  // both warps are past the last tile's exchange
+    if (hi_row) red[ch * kF8Heads + hd] = l;
+    named_bar_sync(2 + qd, 64);
+    if (ch == 0 && hi_row) {
+      const float sum = l + red[kF8Heads + hd];
+      const float inv = sum == 0.f ? 0.f : (1.f / 256.f) / sum;  // P's E4M3 value is 2^8 times its fp16 one
+      fin[h0 + hd] = inv;
+      if (kPair)
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_map(smem_u32(&fin[h0 + hd]), peer)), "f"(inv) : "memory");
+      if (hd < live)
+        lse_part[((size_t)b * n_split + split) * n_heads + h0 + hd] =
+            sum == 0.f ? -INFINITY : (m_ref + log2f(sum)) * 0.6931471805599453f;
     }
-    wait(smem_u32(&bars->p_free), (n_tiles - 1) & 1, ab);
+    wait_cluster(smem_u32(&bars->p_free), (n_tiles - 1) & 1, ab);
     tc_fence_after();
-    named_bar_sync(1, kAll);
-    constexpr uint32_t kRow = kDl * 2 + 16;
+  }
+
+  // Both CTAs' sums are in place, and neither touches the other's memory again
+  // (after a timed-out wait, pushes and arrivals may still be on their way).
+  if (kPair) {
+    if (*ab.flag) {
+      const uint64_t t0 = global_timer_ns();
+      while (global_timer_ns() - t0 < 2000000ull) {
+      }
+    }
+    __syncwarp();
+    cluster_sync();
+  }
+  __syncthreads();
+
+  if (warp < kF8SoftmaxWarps) {
+    // O normalised and turned round through the idle blocks (a head's columns
+    // contiguous), one bulk copy a head.
+    const uint32_t lane_base = (uint32_t)(qd * 32) << 16;
+    constexpr int kWidth = kOwn * 128;
+    constexpr uint32_t kRow = kWidth * 2 + 64;  // rows of two heads fall on the two halves of the banks
 #pragma unroll 1
-    for (int cc = 0; cc < 4; ++cc) {
-      const int m = 2 * hh + (cc >> 1), hb = (cc & 1) * 32;
-      uint32_t ov[32];
-      tmem_ld32(tmem + lane_base + kF8ColO + m * 64 + hb, ov);
+    for (int cc = 0; cc < 8; ++cc) {
+      const int c0 = 128 * ch + 16 * cc, m = c0 / kCols, hb = c0 % kCols;
+      uint32_t ov[16];
+      tmem_ld16(tmem + lane_base + kF8ColO + c0, ov);
       tmem_wait_ld();
-      const uint32_t dst = s0 + (uint32_t)(m * 128 + row) * 2u;
+      // Of two heads, an even lane takes the first and its neighbour the
+      // second: two latent columns in one word.
+      const uint32_t dst = s0 + (uint32_t)(hb + (lane & 1)) * kRow + (uint32_t)(m * 128 + 32 * qd + (lane & ~1)) * 2u;
+      const float4* f4 = reinterpret_cast<const float4*>(fin + hb);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const __nv_bfloat16 v = __float2bfloat16_rn(__uint_as_float(ov[i]) * alpha[hb + i]);
-        asm volatile("st.shared.b16 [%0], %1;" ::"r"(dst + (uint32_t)(hb + i) * kRow), "h"(__bfloat16_as_ushort(v))
-                     : "memory");
+      for (int i = 0; i < 4; ++i) {
+        const float4 f = f4[i];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const float x = __uint_as_float(ov[4 * i + 2 * u]) * (u ? f.z : f.x);
+          const float y = __uint_as_float(ov[4 * i + 2 * u + 1]) * (u ? f.w : f.y);
+          const float other = __shfl_xor_sync(0xffffffffu, (lane & 1) ? x : y, 1);
+          const uint32_t w = (lane & 1) ? pack_bf16x2(other, y) : pack_bf16x2(x, other);
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + (uint32_t)(4 * i + 2 * u) * kRow), "r"(w) : "memory");
+        }
       }
     }
     fence_proxy_async_smem();
-    named_bar_sync(1, kAll);
-    if (tid < live) {
-      bulk_store(o_part + (((size_t)b * n_split + split) * n_heads + h0 + tid) * kDl, s0 + tid * kRow, kDl * 2);
+    named_bar_sync(1, kSoftmaxThreads);
+    if (tid < kCols && tid < n_heads) {
+      bulk_store(o_part + (((size_t)b * n_split + split) * n_heads + tid) * kDl + rank * 256, s0 + tid * kRow, kWidth * 2);
       bulk_commit();
       bulk_wait_read();
     }

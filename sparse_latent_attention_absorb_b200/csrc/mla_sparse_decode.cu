@@ -41,6 +41,13 @@ struct DeviceInfo {
 std::mutex g_mutex;
 DeviceInfo g_dev[kMaxDevices];
 
+cudaError_t configure_attend_fp8() {
+  constexpr auto kAttr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  cudaError_t e = cudaFuncSetAttribute(sparse_attend_fp8_kernel<true>, kAttr, kF8SmemBytes);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(sparse_attend_fp8_kernel<false>, kAttr, kF8SmemBytes);
+  return e;
+}
+
 int current_device(DeviceInfo** info) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return MLA_ERR_CUDA;
@@ -57,7 +64,7 @@ int current_device(DeviceInfo** info) {
     if (d.sm100) {
       if (cudaFuncSetAttribute(absorb_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAbsorbSmemBytes) != cudaSuccess ||
           cudaFuncSetAttribute(sparse_attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttendSmemBytes) != cudaSuccess ||
-          cudaFuncSetAttribute(sparse_attend_fp8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kF8SmemBytes) != cudaSuccess ||
+          configure_attend_fp8() != cudaSuccess ||
           cudaFuncSetAttribute(combine_value_up_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCombineSmemBytes) != cudaSuccess ||
           cudaFuncSetAttribute(projection_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, proj_smem_max()) != cudaSuccess ||
           cudaFuncSetAttribute(check_indices_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -124,14 +131,14 @@ int encode_q_nope(CUtensorMap* m, const void* q_nope, int B, int n_tile, int n_h
 }
 
 // A per-head query tensor (q_lat: width 512, or q_pe: width 64) as a 3-D bf16
-// tensor {c: width, h: n_heads, b: B}, boxes of `box_c` columns x 128 heads x
-// 1 row: one box is a column block of all heads of a row (heads past n_heads
-// lie outside the tensor and read as zero).
+// tensor {c: width, h: n_heads, b: B}, boxes of `box_c` columns x `box_h`
+// heads x 1 row: with all 128 heads one box is a column block of all heads of a
+// row (heads past n_heads lie outside the tensor and read as zero).
 int encode_q_half(CUtensorMap* m, const void* q, int B, int n_heads, int width, int box_c,
-                  CUtensorMapSwizzle swizzle) {
+                  CUtensorMapSwizzle swizzle, int box_h = kH) {
   cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)n_heads, (cuuint64_t)B};
   cuuint64_t strides[2] = {(cuuint64_t)width * 2, (cuuint64_t)n_heads * width * 2};
-  cuuint32_t box[3] = {(cuuint32_t)box_c, (cuuint32_t)kH, 1};
+  cuuint32_t box[3] = {(cuuint32_t)box_c, (cuuint32_t)box_h, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, estr,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
@@ -218,13 +225,13 @@ void plan_splits(int B, int K, int sm_count, int* n_split, int* span) {
   *n_split = ceil_div(K, sp);
 }
 
-// The same over the 8-bit cache: one CTA per (row, split, group of 64 heads),
-// splits of whole 128-slot tiles.
-int fp8_groups(int n_heads) { return ceil_div(n_heads, kF8Heads); }
+// The same over the 8-bit cache: a pair of CTAs per (row, split) for more than
+// 64 heads, one CTA for fewer; splits of whole 128-slot tiles.
+int fp8_ctas(int n_heads) { return n_heads > kF8Heads ? 2 : 1; }
 
 void plan_splits_fp8(int R, int K, int n_heads, int sm_count, int* n_split, int* span) {
   const int tiles = ceil_div(K, kF8Nt);
-  long long want = sm_count / ((long long)R * fp8_groups(n_heads));
+  long long want = sm_count / ((long long)R * fp8_ctas(n_heads));
   if (want < 1) want = 1;
   if (want > tiles) want = tiles;
   if (want > kCombineMaxSplits) want = kCombineMaxSplits;
@@ -297,27 +304,43 @@ WorkspaceLayout workspace_layout(int B, int n_split, int n_heads = kH) {
 int launch_check() { return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA; }
 
 // Launch with or without a programmatic dependency on the previous kernel in
-// the stream.  With one, the kernel may start before that kernel has finished
-// and must call grid_dep_wait() before it reads anything the other writes; the
-// decode step uses it only between its own kernels.
+// the stream, as clusters of `cluster` CTAs along x (0: as the kernel's own
+// attribute says).  With a dependency the kernel may start before that kernel
+// has finished and must call grid_dep_wait() before it reads anything the
+// other writes; the decode step uses it only between its own kernels.
 template <typename... KArgs, typename... Args>
-int launch_ex(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, bool pdl,
-              Args... args) {
+int launch_cluster(void (*kernel)(KArgs...), unsigned cluster, dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                   bool pdl, Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[2];
+  unsigned n = 0;
+  if (pdl) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (cluster > 0) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = cluster;
+    attr[n].val.clusterDim.y = 1;
+    attr[n++].val.clusterDim.z = 1;
+  }
   cfg.attrs = attr;
-  cfg.numAttrs = pdl ? 1 : 0;
+  cfg.numAttrs = n;
   if (cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...) != cudaSuccess) {
     cudaGetLastError();
     return MLA_ERR_CUDA;
   }
   return launch_check();
+}
+
+template <typename... KArgs, typename... Args>
+int launch_ex(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, bool pdl,
+              Args... args) {
+  return launch_cluster(kernel, 0, grid, block, smem, stream, pdl, args...);
 }
 
 int launch_absorb(const void* q_nope, const void* wkv_b, void* q_lat, int B, int* d_status, cudaStream_t stream,
@@ -353,16 +376,23 @@ int launch_attend_fp8(const void* q_lat, const void* q_pe, const void* kv_fp8, c
                       int shift, const int32_t* cache_slot, const int32_t* end_pos, const int32_t* topk_idx,
                       float scale, void* o_part, float* lse_part, int R, int K, int S_max, int n_slots, int n_heads,
                       int n_split, int span, const void* w_next, int* d_status, cudaStream_t stream, bool pdl) {
-  const int groups = fp8_groups(n_heads);
-  const long long ctas = (long long)R * n_split * groups;
+  const int per = fp8_ctas(n_heads);
+  const long long ctas = (long long)R * n_split * per;
   if (ctas > 0x7fffffffLL) return MLA_ERR_INVALID_ARG;
   const int n_blocks = ((S_max - 1) >> shift) + 1;
-  return launch_ex(sparse_attend_fp8_kernel, dim3((unsigned)ctas), dim3(kF8Threads), kF8SmemBytes, stream, pdl,
-                   static_cast<const __nv_bfloat16*>(q_lat), static_cast<const __nv_bfloat16*>(q_pe),
-                   static_cast<const uint8_t*>(kv_fp8), static_cast<const __nv_bfloat16*>(pe), kv_scale, shift,
-                   n_blocks, end_pos, topk_idx, scale, static_cast<__nv_bfloat16*>(o_part), lse_part, K, S_max,
-                   n_split, span, static_cast<const __nv_bfloat16*>(w_next), cache_slot, n_slots, n_heads, groups,
-                   d_status);
+  CUtensorMap tm_q;
+  int rc;
+  if ((rc = encode_q_half(&tm_q, q_lat, R, n_heads, kDl, 64, CU_TENSOR_MAP_SWIZZLE_128B, kF8Heads)) != MLA_OK) return rc;
+  auto go = [&](auto kernel) {
+    return launch_cluster(kernel, (unsigned)per, dim3((unsigned)ctas), dim3(kF8Threads), kF8SmemBytes, stream, pdl,
+                          tm_q, static_cast<const __nv_bfloat16*>(q_pe),
+                          static_cast<const uint8_t*>(kv_fp8), static_cast<const __nv_bfloat16*>(pe), kv_scale, shift,
+                          n_blocks, end_pos, topk_idx, scale, static_cast<__nv_bfloat16*>(o_part), lse_part, K, S_max,
+                          n_split, span, static_cast<const __nv_bfloat16*>(w_next), cache_slot, n_slots, n_heads,
+                          d_status);
+  };
+  return per == 2 ? go(sparse_attend_fp8_kernel<true>)
+                  : go(sparse_attend_fp8_kernel<false>);
 }
 
 int launch_combine(const void* o_part, const float* lse_part, const void* wkv_b, void* out, float* lse_out, int B,
