@@ -474,6 +474,78 @@ int mla_sparse_attend_fp8(const void* q_lat, const void* q_pe, const void* kv_fp
                           int n_slots, int n_heads, int n_split, int* d_status, cudaStream_t stream);
 
 /*
+ * New tokens into the 8-bit cache (the pages' cache writer is not on them).  N
+ * rows of n_seq sequences, one sequence after the other:
+ *   kv_new    bf16 [N,512]  normalised latents c^KV
+ *   pe_new    bf16 [N,64]   rotated rotary keys k^R
+ *   cu_rows   int32 [n_seq+1]  sequence q's rows are [cu_rows[q],
+ *             cu_rows[q+1]); it does not fall.  Rows behind cu_rows[n_seq] are
+ *             ignored (a padded batch)
+ *   start_pos int32 [n_seq]  position of a sequence's first row
+ *   cache_slot optional int32 [n_seq]: the sequences' slots (NULL: sequence q
+ *             writes slot q, and n_slots >= n_seq)
+ *   kv_fp8, pe, kv_scale  the cache (see mla_sparse_decode_fp8), written.  A
+ *             row whose position or slot lies outside the cache is not
+ * A block of positions gets the smallest power of two s with |kv| <= 448 s over
+ * its rows (at least 2^-40); codes are kv / s rounded to E4M3 (nearest, ties to
+ * even), pe becomes pe_new / s in bf16.  Positions of a block before a
+ * sequence's first row are taken to hold rows: s is then at least their scale,
+ * and where it has to grow they are rounded again to it.  Positions behind the
+ * last row are not touched.  Infinite and NaN latents become NaN and do not
+ * count for s.  16-byte aligned pointers.  Two sequences of a call, or two
+ * calls that overlap on the GPU, may not write the same block.  Returns an
+ * mla_status.
+ */
+int mla_append_fp8(const void* kv_new, const void* pe_new, const int32_t* cu_rows, const int32_t* start_pos,
+                   const int32_t* cache_slot, void* kv_fp8, void* pe, float* kv_scale, int block, int N, int n_seq,
+                   int S_max, int n_slots, cudaStream_t stream);
+
+/*
+ * The attention weights of a decode step, summed over the heads and added to
+ * running totals (no counterpart on the pages: mla_evict goes by them):
+ *   acc[b,t] += sum_h exp(score[b,h,t] - lse[b,h])   for the selected t of row b
+ *   q_lat bf16 [B,n_heads,512] (mla_absorb_q), q_pe bf16 [B,n_heads,64], the
+ *         caches, end_pos, topk_idx, scale: as the decode step was given them
+ *         (row b reads slot b); n_heads 1 to 128
+ *   lse   f32 [B,n_heads], the decode step's lse_out
+ *   acc   f32 [B,S_max], read and written at the selected positions only
+ * A position's total gets one addition a call (valid indices are distinct), so
+ * results are reproducible.  Scores and weights are f32.  Returns an mla_status.
+ */
+int mla_accumulate_weights(const void* q_lat, const void* q_pe, const void* kv_cache, const void* pe_cache,
+                           const int32_t* end_pos, const int32_t* topk_idx, float scale, const float* lse, float* acc,
+                           int B, int K, int S_max, int n_heads, int* d_status, cudaStream_t stream);
+int mla_accumulate_weights_fp8(const void* q_lat, const void* q_pe, const void* kv_fp8, const void* pe,
+                               const float* kv_scale, int block, const int32_t* end_pos, const int32_t* topk_idx,
+                               float scale, const float* lse, float* acc, int B, int K, int S_max, int n_heads,
+                               int* d_status, cudaStream_t stream);
+
+/*
+ * Eviction by accumulated weight (no counterpart on the pages: their cache only
+ * grows).  Row b holds n = min(end_pos[b], S_max) positions.  With n <= keep
+ * all stay.  Otherwise the last `recent` stay and, of the others, the keep -
+ * recent of the largest acc (ties: the lower position stays; a NaN total counts
+ * as the largest).  The kept positions move up in their order:
+ *   kept     int32 [B,keep]  the position that now lies at i, -1 from new_end on
+ *   new_end  int32 [B]       min(n, keep), the row's new end position
+ *   kv_out, pe_out (8-bit cache: and scale_out)  the cache, of the same sizes.
+ *            Rows from new_end on, and scales of blocks without a kept row, are
+ *            left as they were
+ *   acc_out  f32 [B,S_max]   the kept positions' totals, zeros behind them
+ * Either every output is its input (in place) or none overlaps it.  A block of
+ * the 8-bit cache gets the largest scale of the rows that it now holds, and
+ * rows of a smaller one are rounded again.  1 <= keep <= S_max, 0 <= recent <=
+ * keep, B <= 65535; 16-byte aligned pointers.  What else is kept by position
+ * (an indexer's keys) moves by `kept`.  Returns an mla_status.
+ */
+int mla_evict(const void* kv_cache, const void* pe_cache, const float* acc, const int32_t* end_pos, void* kv_out,
+              void* pe_out, float* acc_out, int32_t* kept, int32_t* new_end, int B, int S_max, int keep, int recent,
+              cudaStream_t stream);
+int mla_evict_fp8(const void* kv_fp8, const void* pe, const float* kv_scale, int block, const float* acc,
+                  const int32_t* end_pos, void* kv_out, void* pe_out, float* scale_out, float* acc_out, int32_t* kept,
+                  int32_t* new_end, int B, int S_max, int keep, int recent, cudaStream_t stream);
+
+/*
  * Self-test of the bounded waits every kernel relies on (no counterpart on the
  * pages): launches one CTA whose thread waits, through the kernels' own wait,
  * on a barrier that nothing arrives on.  After the wait limit (2 s) it must

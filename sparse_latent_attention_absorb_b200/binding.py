@@ -32,7 +32,8 @@ EXPORTS = ("mla_status_string", "mla_num_splits", "mla_sparse_decode_workspace_s
            "mla_output_projection_shard_workspace_size", "mla_output_projection_shard", "mla_dequant_fp8_blocks",
            "mla_prepare_wo", "mla_output_projection_prepared",
            "mla_num_splits_fp8", "mla_sparse_decode_fp8_workspace_size", "mla_sparse_decode_fp8",
-           "mla_sparse_attend_fp8")
+           "mla_sparse_attend_fp8", "mla_append_fp8", "mla_accumulate_weights", "mla_accumulate_weights_fp8",
+           "mla_evict", "mla_evict_fp8")
 STATIC_SCRATCH_BYTES = 32 << 20  # MLA_STATIC_SCRATCH_BYTES
 
 _lib = None
@@ -111,6 +112,16 @@ def load_library():
     lib.mla_sparse_decode_fp8.argtypes = [p, p, p, p, p, i, p, p, p, p, f, p, i, i, i, i, i, p, sz, p, p, p]
     lib.mla_sparse_attend_fp8.restype = i
     lib.mla_sparse_attend_fp8.argtypes = [p, p, p, p, p, i, p, p, p, f, p, p, i, i, i, i, i, i, p, p]
+    lib.mla_append_fp8.restype = i
+    lib.mla_append_fp8.argtypes = [p, p, p, p, p, p, p, p, i, i, i, i, i, p]
+    lib.mla_accumulate_weights.restype = i
+    lib.mla_accumulate_weights.argtypes = [p, p, p, p, p, p, f, p, p, i, i, i, i, p, p]
+    lib.mla_accumulate_weights_fp8.restype = i
+    lib.mla_accumulate_weights_fp8.argtypes = [p, p, p, p, p, i, p, p, f, p, p, i, i, i, i, p, p]
+    lib.mla_evict.restype = i
+    lib.mla_evict.argtypes = [p, p, p, p, p, p, p, p, p, i, i, i, i, p]
+    lib.mla_evict_fp8.restype = i
+    lib.mla_evict_fp8.argtypes = [p, p, p, i, p, p, p, p, p, p, p, p, i, i, i, i, p]
     lib.mla_selftest_wait_timeout.restype = i
     lib.mla_selftest_wait_timeout.argtypes = [p, p, p]
     _lib = lib
@@ -731,6 +742,144 @@ def mla_sparse_attend_fp8(q_lat, q_pe, cache: Fp8Cache, end_pos, topk_idx, scale
                                    n_split, _ptr(d_status), _stream(stream))
     _raise(rc, "mla_sparse_attend_fp8")
     return o_part, lse_part
+
+
+def mla_append_fp8(cache: Fp8Cache, kv_new, pe_new, cu_rows, start_pos, cache_slot=None, stream=None):
+    """New tokens into an 8-bit cache, in place: rows cu_rows[q] ..
+    cu_rows[q+1] of kv_new (bf16 [N, 512]) and pe_new (bf16 [N, 64]) go to
+    positions start_pos[q] .. of slot q (or cache_slot[q]); returns the
+    cache."""
+    lib = load_library()
+    N, n_seq = kv_new.shape[0], start_pos.shape[0]
+    _check(kv_new, "kv_new", torch.bfloat16, (N, D_LAT))
+    _check(pe_new, "pe_new", torch.bfloat16, (N, D_ROPE))
+    _check(cu_rows, "cu_rows", torch.int32, (n_seq + 1,))
+    _check(start_pos, "start_pos", torch.int32, (n_seq,))
+    if cache_slot is not None:
+        _check(cache_slot, "cache_slot", torch.int32, (n_seq,))
+    _check_same_device(kv_new.device, pe_new=pe_new, cu_rows=cu_rows, start_pos=start_pos, cache_slot=cache_slot,
+                       cache=cache.kv)
+    if N == 0 or n_seq == 0:
+        return cache
+    rc = lib.mla_append_fp8(_ptr(kv_new), _ptr(pe_new), _ptr(cu_rows), _ptr(start_pos), _ptr(cache_slot),
+                            _ptr(cache.kv), _ptr(cache.pe), _ptr(cache.scale), cache.block, N, n_seq, cache.S_max,
+                            cache.n_slots, _stream(stream))
+    _raise(rc, "mla_append_fp8")
+    return cache
+
+
+def _check_weights(q_lat, q_pe, end_pos, topk_idx, lse, acc, S_max, cache, d_status):
+    B, n_heads = q_lat.shape[0], q_lat.shape[1]
+    _check(q_lat, "q_lat", torch.bfloat16, (B, n_heads, D_LAT))
+    _check(q_pe, "q_pe", torch.bfloat16, (B, n_heads, D_ROPE))
+    _check(end_pos, "end_pos", torch.int32, (B,))
+    _check(topk_idx, "topk_idx", torch.int32, (B, topk_idx.shape[1]))
+    _check(lse, "lse", torch.float32, (B, n_heads))
+    _check(acc, "acc", torch.float32, (B, S_max))
+    if d_status is not None:
+        _check(d_status, "d_status", torch.int32, (1,))
+    _check_same_device(q_lat.device, q_pe=q_pe, end_pos=end_pos, topk_idx=topk_idx, lse=lse, acc=acc, cache=cache,
+                       d_status=d_status)
+    return B, topk_idx.shape[1], n_heads
+
+
+def mla_accumulate_weights(q_lat, q_pe, kv_cache, pe_cache, end_pos, topk_idx, scale, lse, acc, d_status=None,
+                           stream=None):
+    """Adds the attention weight of every selected position, summed over the
+    heads, to acc (f32 [B, S_max], in place); q_lat from mla_absorb_q, lse the
+    decode step's lse_out.  Returns acc."""
+    lib = load_library()
+    S_max = kv_cache.shape[1]
+    B, K, n_heads = _check_weights(q_lat, q_pe, end_pos, topk_idx, lse, acc, S_max, kv_cache, d_status)
+    _check(kv_cache, "kv_cache", torch.bfloat16, (B, S_max, D_LAT))
+    _check(pe_cache, "pe_cache", torch.bfloat16, (B, S_max, D_ROPE))
+    rc = lib.mla_accumulate_weights(_ptr(q_lat), _ptr(q_pe), _ptr(kv_cache), _ptr(pe_cache), _ptr(end_pos),
+                                    _ptr(topk_idx), float(scale), _ptr(lse), _ptr(acc), B, K, S_max, n_heads,
+                                    _ptr(d_status), _stream(stream))
+    _raise(rc, "mla_accumulate_weights")
+    return acc
+
+
+def mla_accumulate_weights_fp8(q_lat, q_pe, cache: Fp8Cache, end_pos, topk_idx, scale, lse, acc, d_status=None,
+                               stream=None):
+    """mla_accumulate_weights over an 8-bit cache (row b reads slot b)."""
+    lib = load_library()
+    B, K, n_heads = _check_weights(q_lat, q_pe, end_pos, topk_idx, lse, acc, cache.S_max, cache.kv, d_status)
+    if cache.n_slots < B:
+        raise ValueError(f"cache: {cache.n_slots} slots for {B} rows")
+    rc = lib.mla_accumulate_weights_fp8(_ptr(q_lat), _ptr(q_pe), _ptr(cache.kv), _ptr(cache.pe), _ptr(cache.scale),
+                                        cache.block, _ptr(end_pos), _ptr(topk_idx), float(scale), _ptr(lse),
+                                        _ptr(acc), B, K, cache.S_max, n_heads, _ptr(d_status), _stream(stream))
+    _raise(rc, "mla_accumulate_weights_fp8")
+    return acc
+
+
+def _evict_outputs(acc, end_pos, keep, recent, acc_out, kept, new_end, in_place, **tensors):
+    """Checks what both evictions share; returns (B, S_max, acc_out, kept, new_end)."""
+    if not isinstance(acc, torch.Tensor) or acc.dim() != 2:
+        raise ValueError("acc: expected a tensor [B, S_max]")
+    B, S_max = acc.shape
+    _check(acc, "acc", torch.float32, (B, S_max))
+    _check(end_pos, "end_pos", torch.int32, (B,))
+    for name, v in (("keep", keep), ("recent", recent)):
+        if isinstance(v, bool) or not isinstance(v, int):
+            raise TypeError(f"{name}: expected an int")
+    if not (1 <= keep <= S_max and 0 <= recent <= keep):
+        raise ValueError(f"expected 1 <= keep <= {S_max} and 0 <= recent <= keep, got {keep} and {recent}")
+    if acc_out is None:
+        acc_out = acc if in_place else torch.empty_like(acc)
+    _check(acc_out, "acc_out", torch.float32, (B, S_max))
+    if kept is None:
+        kept = torch.empty((B, keep), dtype=torch.int32, device=acc.device)
+    if new_end is None:
+        new_end = torch.empty(B, dtype=torch.int32, device=acc.device)
+    _check(kept, "kept", torch.int32, (B, keep))
+    _check(new_end, "new_end", torch.int32, (B,))
+    _check_same_device(acc.device, end_pos=end_pos, acc_out=acc_out, kept=kept, new_end=new_end, **tensors)
+    return B, S_max, acc_out, kept, new_end
+
+
+def mla_evict(kv_cache, pe_cache, acc, end_pos, keep: int, recent: int, kv_out=None, pe_out=None, acc_out=None,
+              kept=None, new_end=None, stream=None):
+    """Eviction by accumulated weight: rows longer than `keep` keep their last
+    `recent` positions and those of the largest acc, moved up in their order.
+    In place, or into kv_out, pe_out and acc_out (all or none of them).
+    Returns (kept int32 [B, keep], new_end int32 [B])."""
+    lib = load_library()
+    in_place = kv_out is None
+    if (pe_out is None) != in_place or (in_place and acc_out is not None):
+        raise ValueError("kv_out, pe_out and acc_out: give all of them, or none (in place)")
+    B, S_max, acc_out, kept, new_end = _evict_outputs(acc, end_pos, keep, recent, acc_out, kept, new_end, in_place,
+                                                      kv_cache=kv_cache, pe_cache=pe_cache, kv_out=kv_out,
+                                                      pe_out=pe_out)
+    kv_out, pe_out = (kv_cache, pe_cache) if in_place else (kv_out, pe_out)
+    for name, t, d in (("kv_cache", kv_cache, D_LAT), ("pe_cache", pe_cache, D_ROPE), ("kv_out", kv_out, D_LAT),
+                       ("pe_out", pe_out, D_ROPE)):
+        _check(t, name, torch.bfloat16, (B, S_max, d))
+    rc = lib.mla_evict(_ptr(kv_cache), _ptr(pe_cache), _ptr(acc), _ptr(end_pos), _ptr(kv_out), _ptr(pe_out),
+                       _ptr(acc_out), _ptr(kept), _ptr(new_end), B, S_max, keep, recent, _stream(stream))
+    _raise(rc, "mla_evict")
+    return kept, new_end
+
+
+def mla_evict_fp8(cache: Fp8Cache, acc, end_pos, keep: int, recent: int, cache_out: Fp8Cache = None, acc_out=None,
+                  kept=None, new_end=None, stream=None):
+    """mla_evict over the first B slots of an 8-bit cache: in place, or into
+    cache_out (of the same S_max and block) and acc_out."""
+    lib = load_library()
+    in_place = cache_out is None
+    if in_place and acc_out is not None:
+        raise ValueError("cache_out and acc_out: give both, or neither (in place)")
+    to = cache if in_place else cache_out
+    B, S_max, acc_out, kept, new_end = _evict_outputs(acc, end_pos, keep, recent, acc_out, kept, new_end, in_place,
+                                                      cache=cache.kv, cache_out=to.kv)
+    if (cache.S_max, to.S_max) != (S_max, S_max) or cache.block != to.block or min(cache.n_slots, to.n_slots) < B:
+        raise ValueError(f"cache, cache_out: expected at least {B} slots of {S_max} positions and one block size")
+    rc = lib.mla_evict_fp8(_ptr(cache.kv), _ptr(cache.pe), _ptr(cache.scale), cache.block, _ptr(acc), _ptr(end_pos),
+                           _ptr(to.kv), _ptr(to.pe), _ptr(to.scale), _ptr(acc_out), _ptr(kept), _ptr(new_end), B,
+                           S_max, keep, recent, _stream(stream))
+    _raise(rc, "mla_evict_fp8")
+    return kept, new_end
 
 
 def host_input_buffer(B: int, K: int, S_max: int):

@@ -58,18 +58,19 @@ __device__ __forceinline__ int limb_exponent(float amax) {
 }
 __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }  // |e| <= 126
 
-// Four bf16 query factors x as limbs: x 2^e = hi + lo / 16, `mul` = 2^(e - 8).
-// The second limb is scaled by 16 so that it keeps its bits however small x is:
-// a bf16 x is met exactly (4 + 4 signed bits) down to 2^-17 of the largest.
+// Four bf16 query factors x as limbs: x 2^e = hi + lo / lo_scale, `mul` =
+// 2^(e - 8).  A second limb that is scaled up by 16 keeps its bits however small
+// x is: a bf16 x is met exactly (4 + 4 signed bits) down to 2^-17 of the
+// largest; one that is not, down to 2^-10, and to 2^-19 of the largest below.
 constexpr float kLimbLo = 1.f / 16.f;
-__device__ __forceinline__ void limbs4(uint32_t x01, uint32_t x23, float mul, uint32_t* hi, uint32_t* lo) {
+__device__ __forceinline__ void limbs4(uint32_t x01, uint32_t x23, float mul, float lo_scale, uint32_t* hi, uint32_t* lo) {
   uint32_t first[2], rest[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const uint32_t x = i ? x23 : x01;
     const uint32_t f = half2_bits(__floats2half2_rn(__uint_as_float(x << 16) * mul, __uint_as_float(x & 0xffff0000u) * mul));
     first[i] = limb_first(f);
-    rest[i] = limb_first(half2_bits(__hmul2(limb_rest(f, first[i]), __float2half2_rn(16.f))));
+    rest[i] = limb_first(half2_bits(__hmul2(limb_rest(f, first[i]), __float2half2_rn(lo_scale))));
   }
   *hi = limb_bytes(first[0], first[1]);
   *lo = limb_bytes(rest[0], rest[1]);
@@ -558,7 +559,7 @@ sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __nv_bf
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           uint32_t hi, lo;
-          limbs4(u ? v.z : v.x, u ? v.w : v.y, mul * (1.f / 256.f), &hi, &lo);
+          limbs4(u ? v.z : v.x, u ? v.w : v.y, mul * (1.f / 256.f), 1.f / kLimbLo, &hi, &lo);
           const uint32_t other = __shfl_xor_sync(0xffffffffu, hi_row ? lo : hi, 16);
           r[u] = hi_row ? hi : other;
           r[2 + u] = hi_row ? other : lo;

@@ -11,12 +11,15 @@
 #include <cstring>
 #include <mutex>
 
+#include "append_fp8.cuh"
 #include "attend_fp8.cuh"
 #include "dequant.cuh"
+#include "evict.cuh"
 #include "index_check.cuh"
 #include "kernels.cuh"
 #include "mla_sparse_decode.h"
 #include "projection.cuh"
+#include "weights.cuh"
 
 namespace {
 
@@ -41,10 +44,12 @@ struct DeviceInfo {
 std::mutex g_mutex;
 DeviceInfo g_dev[kMaxDevices];
 
-cudaError_t configure_attend_fp8() {
+cudaError_t configure_cache_kernels() {
   constexpr auto kAttr = cudaFuncAttributeMaxDynamicSharedMemorySize;
   cudaError_t e = cudaFuncSetAttribute(sparse_attend_fp8_kernel<true>, kAttr, kF8SmemBytes);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(sparse_attend_fp8_kernel<false>, kAttr, kF8SmemBytes);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(accumulate_weights_kernel<false>, kAttr, kWtSmemBytes);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(accumulate_weights_kernel<true>, kAttr, kWtSmemBytes);
   return e;
 }
 
@@ -64,7 +69,7 @@ int current_device(DeviceInfo** info) {
     if (d.sm100) {
       if (cudaFuncSetAttribute(absorb_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAbsorbSmemBytes) != cudaSuccess ||
           cudaFuncSetAttribute(sparse_attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttendSmemBytes) != cudaSuccess ||
-          configure_attend_fp8() != cudaSuccess ||
+          configure_cache_kernels() != cudaSuccess ||
           cudaFuncSetAttribute(combine_value_up_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCombineSmemBytes) != cudaSuccess ||
           cudaFuncSetAttribute(projection_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, proj_smem_max()) != cudaSuccess ||
           cudaFuncSetAttribute(check_indices_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -729,6 +734,144 @@ extern "C" int mla_sparse_decode_fp8(const void* q_nope, const void* q_pe, const
                               stream, true)) != MLA_OK)
     return rc;
   return launch_combine(o_part, lse_part, wkv_b, out, lse_out, R, n_split, d_status, stream, true, n_heads);
+}
+
+// New tokens into the 8-bit cache (see the header).
+extern "C" int mla_append_fp8(const void* kv_new, const void* pe_new, const int32_t* cu_rows, const int32_t* start_pos,
+                              const int32_t* cache_slot, void* kv_fp8, void* pe, float* kv_scale, int block, int N,
+                              int n_seq, int S_max, int n_slots, cudaStream_t stream) {
+  const void* ptrs[] = {kv_new, pe_new, cu_rows, start_pos};
+  for (const void* p : ptrs)
+    if (!p || !aligned16(p)) return MLA_ERR_INVALID_ARG;
+  if (!fp8_cache_ok(kv_fp8, pe, kv_scale, block, S_max, n_slots) || !slots_ok(cache_slot, n_seq, n_slots))
+    return MLA_ERR_INVALID_ARG;
+  if (N < 1 || N > (1 << 24) || n_seq < 1 || n_seq > kMaxB) return MLA_ERR_INVALID_ARG;
+  DeviceInfo* info = nullptr;
+  int rc = prepare(&info);
+  if (rc != MLA_OK) return rc;
+  const int shift = block_shift(block);
+  const AppendArgs a{static_cast<const __nv_bfloat16*>(kv_new), static_cast<const __nv_bfloat16*>(pe_new), cu_rows,
+                     start_pos, cache_slot, static_cast<uint8_t*>(kv_fp8), static_cast<__nv_bfloat16*>(pe), kv_scale,
+                     N, n_seq, S_max, n_slots, shift, ((S_max - 1) >> shift) + 1};
+  constexpr int kWarps = kAppendThreads / 32;
+  if (shift == 0)
+    return launch_ex(append_fp8_rows_kernel, dim3((unsigned)ceil_div(N, kWarps)), dim3(kAppendThreads), 0, stream,
+                     false, a);
+  // A CTA a token while all of them run at once (a decode step: every token
+  // leads its block); for more, eight tokens a CTA, of which few lead one.
+  const int per = N <= kWarps * info->sm_count ? 1 : kWarps;
+  return launch_ex(append_fp8_blocks_kernel, dim3((unsigned)ceil_div(N, per)), dim3(kAppendThreads), 0, stream, false,
+                   a, per);
+}
+
+// ---------------------------------------------------------------- weights, eviction
+namespace {
+template <bool kFp8>
+int run_weights(const void* q_lat, const void* q_pe, const void* kv, const void* pe, const float* kv_scale, int shift,
+                const int32_t* end_pos, const int32_t* topk_idx, float scale, const float* lse, float* acc, int B, int K,
+                int S_max, int n_heads, int* d_status, cudaStream_t stream) {
+  const void* ptrs[] = {q_lat, q_pe, kv, pe, end_pos, topk_idx, lse, acc};
+  for (const void* p : ptrs)
+    if (!p || !aligned16(p)) return MLA_ERR_INVALID_ARG;
+  if (d_status && (reinterpret_cast<uintptr_t>(d_status) & 3u)) return MLA_ERR_INVALID_ARG;
+  if (!sizes_ok(B, K, S_max) || n_heads < 1 || n_heads > kH || !std::isfinite(scale)) return MLA_ERR_INVALID_ARG;
+  DeviceInfo* info = nullptr;
+  int rc = prepare(&info);
+  if (rc != MLA_OK) return rc;
+  // whole 128-slot tiles, as many splits as fill the SMs
+  const int tiles = ceil_div(K, kWtNt);
+  const int want = B >= info->sm_count ? 1 : (info->sm_count / B < tiles ? info->sm_count / B : tiles);
+  const int span = ceil_div(tiles, want) * kWtNt, n_split = ceil_div(K, span);
+  CUtensorMap tm_q;
+  if ((rc = encode_q_half(&tm_q, q_lat, B, n_heads, kDl, 64, CU_TENSOR_MAP_SWIZZLE_128B)) != MLA_OK) return rc;
+  return launch_ex(accumulate_weights_kernel<kFp8>, dim3((unsigned)(B * n_split)), dim3(kWtThreads), kWtSmemBytes,
+                   stream, false, tm_q, static_cast<const __nv_bfloat16*>(q_pe), static_cast<const uint8_t*>(kv),
+                   static_cast<const uint8_t*>(pe), kv_scale, shift, ((S_max - 1) >> shift) + 1, end_pos, topk_idx,
+                   scale, lse, acc, K, S_max, n_split, span, n_heads, d_status);
+}
+
+bool overlap(const void* a, const void* b, size_t bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + bytes && y < x + bytes;
+}
+
+// Each output is its input (in place) or lies apart from it, all of them alike.
+struct EvictBuffers {
+  const void* in[4];
+  void* out[4];
+  size_t bytes[4];
+  int n;
+};
+
+template <bool kFp8>
+int run_evict(const EvictBuffers& e, const int32_t* end_pos, int32_t* kept, int32_t* new_end, int shift, int B,
+              int S_max, int keep, int recent, cudaStream_t stream) {
+  const void* ptrs[] = {end_pos, kept, new_end};
+  for (const void* p : ptrs)
+    if (!p || !aligned16(p)) return MLA_ERR_INVALID_ARG;
+  if (keep < 1 || keep > S_max || recent < 0 || recent > keep) return MLA_ERR_INVALID_ARG;
+  const bool in_place = e.in[0] == e.out[0];
+  for (int i = 0; i < e.n; ++i) {
+    if (!e.in[i] || !e.out[i] || !aligned16(e.in[i]) || !aligned16(e.out[i])) return MLA_ERR_INVALID_ARG;
+    if (in_place ? e.in[i] != e.out[i] : overlap(e.in[i], e.out[i], e.bytes[i])) return MLA_ERR_INVALID_ARG;
+  }
+  DeviceInfo* info = nullptr;
+  int rc = prepare(&info);
+  if (rc != MLA_OK) return rc;
+  if ((rc = launch_ex(evict_select_kernel, dim3((unsigned)B), dim3(kSelectThreads), 0, stream, false,
+                      static_cast<const float*>(e.in[0]), end_pos, static_cast<float*>(e.out[0]), kept, new_end, S_max,
+                      keep, recent)) != MLA_OK)
+    return rc;
+  const MoveArgs a{static_cast<const uint8_t*>(e.in[1]), static_cast<const uint8_t*>(e.in[2]),
+                   kFp8 ? static_cast<const float*>(e.in[3]) : nullptr, static_cast<uint8_t*>(e.out[1]),
+                   static_cast<uint8_t*>(e.out[2]), kFp8 ? static_cast<float*>(e.out[3]) : nullptr, kept, new_end,
+                   end_pos, S_max, keep, shift, ((S_max - 1) >> shift) + 1};
+  if (in_place)
+    return launch_cluster(evict_move_kernel<kFp8, true>, kMoveCluster, dim3(kMoveCluster, (unsigned)B),
+                          dim3(kMoveThreads), 0, stream, false, a);
+  return launch_ex(evict_move_kernel<kFp8, false>, dim3((unsigned)ceil_div(keep, kMoveRows), (unsigned)B),
+                   dim3(kMoveThreads), 0, stream, false, a);
+}
+constexpr int kMaxEvictRows = 65535;  // grid y
+}  // namespace
+
+extern "C" int mla_accumulate_weights(const void* q_lat, const void* q_pe, const void* kv_cache, const void* pe_cache,
+                                      const int32_t* end_pos, const int32_t* topk_idx, float scale, const float* lse,
+                                      float* acc, int B, int K, int S_max, int n_heads, int* d_status,
+                                      cudaStream_t stream) {
+  return run_weights<false>(q_lat, q_pe, kv_cache, pe_cache, nullptr, 0, end_pos, topk_idx, scale, lse, acc, B, K,
+                            S_max, n_heads, d_status, stream);
+}
+
+extern "C" int mla_accumulate_weights_fp8(const void* q_lat, const void* q_pe, const void* kv_fp8, const void* pe,
+                                          const float* kv_scale, int block, const int32_t* end_pos,
+                                          const int32_t* topk_idx, float scale, const float* lse, float* acc, int B,
+                                          int K, int S_max, int n_heads, int* d_status, cudaStream_t stream) {
+  if (!fp8_cache_ok(kv_fp8, pe, kv_scale, block, S_max, 1)) return MLA_ERR_INVALID_ARG;
+  return run_weights<true>(q_lat, q_pe, kv_fp8, pe, kv_scale, block_shift(block), end_pos, topk_idx, scale, lse, acc,
+                           B, K, S_max, n_heads, d_status, stream);
+}
+
+extern "C" int mla_evict(const void* kv_cache, const void* pe_cache, const float* acc, const int32_t* end_pos,
+                         void* kv_out, void* pe_out, float* acc_out, int32_t* kept, int32_t* new_end, int B, int S_max,
+                         int keep, int recent, cudaStream_t stream) {
+  if (B < 1 || B > kMaxEvictRows || S_max < 1) return MLA_ERR_INVALID_ARG;
+  const size_t rows = (size_t)B * S_max;
+  const EvictBuffers e{{acc, kv_cache, pe_cache, nullptr}, {acc_out, kv_out, pe_out, nullptr},
+                       {rows * 4, rows * kDl * 2, rows * kDr * 2, 0}, 3};
+  return run_evict<false>(e, end_pos, kept, new_end, 0, B, S_max, keep, recent, stream);
+}
+
+extern "C" int mla_evict_fp8(const void* kv_fp8, const void* pe, const float* kv_scale, int block, const float* acc,
+                             const int32_t* end_pos, void* kv_out, void* pe_out, float* scale_out, float* acc_out,
+                             int32_t* kept, int32_t* new_end, int B, int S_max, int keep, int recent,
+                             cudaStream_t stream) {
+  if (B < 1 || B > kMaxEvictRows || !fp8_cache_ok(kv_fp8, pe, kv_scale, block, S_max, 1)) return MLA_ERR_INVALID_ARG;
+  const int shift = block_shift(block);
+  const size_t rows = (size_t)B * S_max, blocks = (size_t)B * (((S_max - 1) >> shift) + 1);
+  const EvictBuffers e{{acc, kv_fp8, pe, kv_scale}, {acc_out, kv_out, pe_out, scale_out},
+                       {rows * 4, rows * kDl, rows * kDr * 2, blocks * 4}, 4};
+  return run_evict<true>(e, end_pos, kept, new_end, shift, B, S_max, keep, recent, stream);
 }
 
 // fp8 block dequantisation (see the header).
