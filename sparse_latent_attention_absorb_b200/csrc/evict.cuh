@@ -9,8 +9,8 @@
 //                        the kept positions; the totals move along
 //   evict_move_kernel    the rows
 //
-// Bound: the select reads a row's totals five times from L1 and L2 with one
-// CTA a row, the move is HBM traffic.
+// Bound: the select reads a row's totals five times from L1 and L2, the move is
+// HBM traffic.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -22,6 +22,8 @@ namespace mla {
 
 constexpr int kSelectThreads = 1024;
 constexpr int kSelectBins = 2048;
+constexpr int kSelectUnroll = 4;  // independent loads of a thread
+constexpr int kSelectCluster = 8;
 
 // Bits whose unsigned order is the weights' order, NaN above all, the two zeros
 // equal.
@@ -57,95 +59,165 @@ __device__ __forceinline__ int2 block_scan2(int2 v, int2* warp_sums, int2* total
   return make_int2(before.x + x.x - v.x, before.y + x.y - v.y);
 }
 
+// A row's CTAs (one, or a cluster of kSelectCluster for long rows) take a run
+// of its positions each; histograms and counts meet through distributed shared
+// memory.
 __global__ void __launch_bounds__(kSelectThreads, 1)
 evict_select_kernel(const float* acc, const int32_t* __restrict__ end_pos, float* acc_out,
-                    int32_t* __restrict__ kept, int32_t* __restrict__ new_end, int S_max, int keep, int recent) {
-  __shared__ uint32_t bins[kSelectBins];
+                    int32_t* kept, int32_t* __restrict__ new_end, int S_max, int keep, int recent) {
+  __shared__ uint32_t bins[kSelectBins], meet[kSelectBins];
   __shared__ int2 warp_sums[32];
   __shared__ uint32_t found[2];
-  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
+  __shared__ int2 counts;
+  const int n_cta = (int)cluster_size(), rank = (int)cluster_ctarank();
+  const int b = blockIdx.x / n_cta, tid = threadIdx.x, lane = tid & 31;
   const float* w = acc + (size_t)b * S_max;
+  float* out = acc_out + (size_t)b * S_max;
+  const bool apart = acc_out != acc;
   int32_t* kp = kept + (size_t)b * keep;
   int n = end_pos[b];
   n = n < 0 ? 0 : (n > S_max ? S_max : n);
   const int n_new = min(n, keep);
   const int late = n - min(recent, keep);  // positions from here on stay (n > keep)
+  const int all = n_cta * kSelectThreads, me = rank * kSelectThreads + tid;
 
   if (n <= keep) {
-    for (int i = tid; i < keep; i += kSelectThreads) kp[i] = i < n ? i : -1;
+    for (int i = me; i < keep; i += all) {
+      kp[i] = i < n ? i : -1;
+      if (apart && i < n) out[i] = w[i];
+    }
   } else {
-    // the key of rank `rank` (from 0, largest first) among [0, late)
+    const int seg = (n + n_cta * 1024 - 1) / (n_cta * 1024) * 1024;  // a CTA's positions
+    const int s0 = min(n, rank * seg), s1 = min(n, s0 + seg);
+    const int l1 = min(s1, late);
+    // the key of rank `left` (from 1, largest first) among [0, late)
     uint32_t prefix = 0, mask = 0;
-    int rank = keep - min(recent, keep);  // how many of [0, late) stay
-    if (rank > 0) {
+    int left = keep - min(recent, keep);  // how many of [0, late) stay
+    if (left > 0) {
 #pragma unroll 1
       for (int pass = 0; pass < 3; ++pass) {
         const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), width = pass == 2 ? 10 : 11;
         for (int i = tid; i < kSelectBins; i += kSelectThreads) bins[i] = 0;
         __syncthreads();
-        for (int i0 = 0; i0 < late; i0 += kSelectThreads) {
-          const int i = i0 + tid;
-          const uint32_t k = i < late ? weight_key(w[i]) : 0u;
-          const bool in = i < late && (k & mask) == prefix;
-          const uint32_t bin = (k >> shift) & ((1u << width) - 1u);
-          // equal weights (never selected: 0) would queue up at one bin: the
-          // lanes that share the first lane's bin count as one
-          const uint32_t act = __ballot_sync(0xffffffffu, in);
-          if (act) {
-            const uint32_t lead = __shfl_sync(0xffffffffu, bin, __ffs(act) - 1);
-            const uint32_t same = __ballot_sync(0xffffffffu, in && bin == lead);
-            if (lane == __ffs(act) - 1)
-              atomicAdd(&bins[lead], (uint32_t)__popc(same));
-            else if (in && bin != lead)
-              atomicAdd(&bins[bin], 1u);
+        for (int i0 = s0; i0 < l1; i0 += kSelectUnroll * kSelectThreads) {
+          float x[kSelectUnroll];
+#pragma unroll
+          for (int u = 0; u < kSelectUnroll; ++u) {
+            const int i = i0 + u * kSelectThreads + tid;
+            x[u] = i < l1 ? w[i] : 0.f;
+          }
+#pragma unroll
+          for (int u = 0; u < kSelectUnroll; ++u) {
+            const uint32_t k = weight_key(x[u]);
+            const bool in = i0 + u * kSelectThreads + tid < l1 && (k & mask) == prefix;
+            const uint32_t bin = (k >> shift) & ((1u << width) - 1u);
+            // equal weights (never selected: 0) would queue up at one bin: the
+            // lanes that share the first lane's bin count as one
+            const uint32_t act = __ballot_sync(0xffffffffu, in);
+            if (act) {
+              const uint32_t lead = __shfl_sync(0xffffffffu, bin, __ffs(act) - 1);
+              const uint32_t same = __ballot_sync(0xffffffffu, in && bin == lead);
+              if (lane == __ffs(act) - 1)
+                atomicAdd(&bins[lead], (uint32_t)__popc(same));
+              else if (in && bin != lead)
+                atomicAdd(&bins[bin], 1u);
+            }
           }
         }
-        __syncthreads();
-        // bins from the top: thread t holds bins 2047 - 2t and 2046 - 2t
+        cluster_sync();
+        // bins from the top, of all CTAs: thread t holds bins 2047 - 2t and 2046 - 2t
         const int b0 = kSelectBins - 1 - 2 * tid;
-        const int c0 = (int)bins[b0], c1 = (int)bins[b0 - 1];
+        const uint32_t* sums = bins;
+        if (n_cta > 1) {
+          // a CTA adds up its share of the bins and tells everyone
+          const int share = kSelectBins / kSelectCluster;
+          if (tid < share) {
+            const uint32_t at = smem_u32(&bins[rank * share + tid]), to = smem_u32(&meet[rank * share + tid]);
+            uint32_t sum = 0;
+#pragma unroll
+            for (int r = 0; r < kSelectCluster; ++r) sum += ld_cluster_u32(cluster_map(at, (uint32_t)r));
+#pragma unroll
+            for (int r = 0; r < kSelectCluster; ++r) st_cluster_u32(cluster_map(to, (uint32_t)r), sum);
+          }
+          cluster_sync();
+          sums = meet;
+        }
+        const int c0 = (int)sums[b0], c1 = (int)sums[b0 - 1];
         int2 total;
         const int before = block_scan2(make_int2(c0 + c1, 0), warp_sums, &total).x;
-        if (before < rank && rank <= before + c0) found[0] = (uint32_t)b0, found[1] = (uint32_t)before;
-        if (before + c0 < rank && rank <= before + c0 + c1) found[0] = (uint32_t)(b0 - 1), found[1] = (uint32_t)(before + c0);
+        if (before < left && left <= before + c0) found[0] = (uint32_t)b0, found[1] = (uint32_t)before;
+        if (before + c0 < left && left <= before + c0 + c1) found[0] = (uint32_t)(b0 - 1), found[1] = (uint32_t)(before + c0);
         __syncthreads();
         prefix |= found[0] << shift;
         mask |= ((1u << width) - 1u) << shift;
-        rank -= (int)found[1];
-        __syncthreads();
+        left -= (int)found[1];
       }
     } else {
       prefix = 0xffffffffu;  // no key is larger, and none of the ties stays
     }
-    // Above the key, or one of its first `rank` ties, or late: a thread takes
-    // a run of positions, so that one scan numbers them all.
-    const int run = (n + kSelectThreads - 1) / kSelectThreads;
-    const int i0 = min(n, tid * run), i1 = min(n, i0 + run);
+    // Above the key, or one of its first `left` ties, or late.  A warp takes
+    // 1/32 of the CTA's positions, 32 at a time, and counts them; the sums over
+    // the warps and CTAs before it tell it where its own go.
+    const int run = seg / 32;
+    const int i0 = min(s1, s0 + (tid >> 5) * run), i1 = min(s1, i0 + run);
+    // the lanes of a step whose position is above the key, and its ties
+    auto look = [&](float x, int i, uint32_t* above, uint32_t* ties) {
+      const uint32_t k = weight_key(x);
+      *above = __ballot_sync(0xffffffffu, i < i1 && (i >= late || k > prefix));
+      *ties = __ballot_sync(0xffffffffu, i < i1 && i < late && k == prefix);
+    };
+    auto load = [&](float (&x)[kSelectUnroll], int i) {
+#pragma unroll
+      for (int u = 0; u < kSelectUnroll; ++u) x[u] = i + 32 * u + lane < i1 ? w[i + 32 * u + lane] : 0.f;
+    };
     int2 c = make_int2(0, 0);
-    for (int i = i0; i < i1; ++i) {
-      const uint32_t k = i < late ? weight_key(w[i]) : 0u;
-      c.x += i >= late || k > prefix;
-      c.y += i < late && k == prefix;
+    for (int i = i0; i < i1; i += 32 * kSelectUnroll) {
+      float x[kSelectUnroll];
+      load(x, i);
+#pragma unroll
+      for (int u = 0; u < kSelectUnroll; ++u) {
+        uint32_t above, ties;
+        look(x[u], i + 32 * u + lane, &above, &ties);
+        c.x += __popc(above), c.y += __popc(ties);
+      }
     }
     int2 total;
-    int2 at = block_scan2(c, warp_sums, &total);
-    for (int i = i0; i < i1; ++i) {
-      const uint32_t k = i < late ? weight_key(w[i]) : 0u;
-      const bool tie = i < late && k == prefix;
-      const bool stays = i >= late || k > prefix || (tie && at.y < rank);
-      // positions above the key before i, and the ties among them that stay
-      if (stays) kp[at.x + min(at.y, rank)] = i;
-      at.x += i >= late || k > prefix;
-      at.y += tie;
+    int2 at = block_scan2(lane == 31 ? c : make_int2(0, 0), warp_sums, &total);
+    at.x = __shfl_sync(0xffffffffu, at.x, 0), at.y = __shfl_sync(0xffffffffu, at.y, 0);
+    if (tid == 0) counts = total;
+    cluster_sync();
+    for (int r = 0; r < rank; ++r) {
+      const uint32_t far = cluster_map(smem_u32(&counts), (uint32_t)r);
+      at.x += (int)ld_cluster_u32(far), at.y += (int)ld_cluster_u32(far + 4);
+    }
+    const uint32_t below = (1u << lane) - 1u;
+    for (int i = i0; i < i1; i += 32 * kSelectUnroll) {
+      float x[kSelectUnroll];
+      load(x, i);
+#pragma unroll
+      for (int u = 0; u < kSelectUnroll; ++u) {
+        uint32_t above, ties;
+        look(x[u], i + 32 * u + lane, &above, &ties);
+        const int tie = at.y + __popc(ties & below);
+        // positions above the key before this one, and the ties among them that stay
+        const int to = at.x + __popc(above & below) + min(tie, left);
+        if ((above >> lane & 1u) || ((ties >> lane & 1u) && tie < left)) {
+          kp[to] = i + 32 * u + lane;
+          if (apart) out[to] = x[u];
+        }
+        at.x += __popc(above), at.y += __popc(ties);
+      }
     }
   }
-  if (tid == 0) new_end[b] = n_new;
-  __syncthreads();
-  // The totals of the kept positions, then zeros.  acc_out may be acc: what a
-  // step writes, [i0, i0 + 1024), no later step reads, and its own reads are
-  // done.
-  float* out = acc_out + (size_t)b * S_max;
-  for (int i0 = 0; i0 < n_new; i0 += kSelectThreads) {
+  if (me == 0) new_end[b] = n_new;
+  if (apart) {
+    for (int i = n_new + me; i < S_max; i += all) out[i] = 0.f;
+  }
+  cluster_sync();  // kept is whole, and no CTA reads another's memory any more
+  if (apart || rank != 0) return;
+  // In place, one CTA: what a step writes, [i0, i0 + 1024), no later step
+  // reads, and its own reads are done.
+  for (int i0 = 0; n > keep && i0 < n_new; i0 += kSelectThreads) {
     const int i = i0 + tid;
     const float v = i < n_new ? w[kp[i]] : 0.f;
     __syncthreads();
@@ -189,9 +261,10 @@ __global__ void __launch_bounds__(kMoveThreads, 1) evict_move_kernel(const MoveA
   const int32_t* kept = a.kept + (size_t)b * a.keep;
   const size_t row0 = (size_t)b * a.S_max;
   const int block = 1 << a.shift;
-  const int step = kInPlace ? kMoveCluster * kMoveRows : kMoveRows;
-  for (int base = kInPlace ? 0 : blockIdx.x * kMoveRows; base < n; base += step) {
-    const int i0 = kInPlace ? base + (int)blockIdx.x * kMoveRows : base;
+  const int step = (int)gridDim.x * kMoveRows;  // out of place: the grid covers `keep`, one step
+  for (int base = 0; base < n; base += step) {
+    const int i0 = base + (int)blockIdx.x * kMoveRows;
+    if (!kInPlace && i0 >= n) break;
     if (kInPlace) {
       const int last = min(base + step, n) - 1;
       if (kept[last] == last) continue;  // nothing has moved up to here
