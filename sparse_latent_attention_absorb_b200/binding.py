@@ -133,8 +133,9 @@ def _ptr(t):
 
 
 def _stream(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    if stream is None:  # the raw handle: building a Stream object costs several microseconds
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _check(t: torch.Tensor, name: str, dtype, shape=None):
@@ -651,6 +652,8 @@ class Fp8Cache:
 
 
 def _check_same_device(device, **tensors):
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {device}, but the current device is cuda:{torch.cuda.current_device()}")
     for name, t in tensors.items():
         if t is not None and t.device != device:
             raise ValueError(f"{name}: on {t.device}, expected {device}")
