@@ -108,31 +108,36 @@ __device__ __forceinline__ uint32_t amax2(uint32_t m, uint32_t x) { return __vma
 // m_h is the largest y of some tile plus a margin, and moves only when P would
 // leave E4M3's range; the softmax warps then rescale the columns of O of the
 // heads it moved for between two PVs, in both CTAs of a pair (which tell each
-// other as soon as they know, while P is being formed).
+// other as soon as they know; P does not wait for that, only PV does).
 //
 // Shared memory: blocks of 16 KB (128 positions x 128 bytes, 128-byte swizzle).
-//   Pair:   a ring of four for what only QK reads (rotary rows, the peer's
-//           columns), three stages of the CTA's own columns (two blocks each,
-//           held until PV has read them), P (two limbs of 128 heads).
-//   Single: a ring of two for the rotary rows, two stages of four blocks, P.
-// The tile's time is set by how far the gather runs ahead: with two stages and
-// one set of the peer's columns it took 4000 cycles, of about 2400 of MMA.
+//   Pair:   three for what only QK reads (rotary rows, the peer's columns),
+//           three stages of the CTA's own columns (two blocks each, held until
+//           PV has read them), three limbs of P of 128 heads.
+//   Single: a ring of two for the rotary rows, two stages of four blocks, two
+//           buffers of P.
 //
-// Warps (480 threads): 0-7 softmax (warp w: TMEM lanes 32 (w % 4).., positions
+// Warps (512 threads): 0-7 softmax (warp w: TMEM lanes 32 (w % 4).., positions
 // 64 (w / 4)..), 8-11 gather (one on each sub-partition of the SM: two warps on
-// two of them took 4900 cycles a tile), 12 query load and QK issue, 13 TMEM, PV
-// issue and pushes, 14 positions, scales and L2 prefetch.
+// two of them took 4900 cycles a tile), 12 query load and QK issue, 13 TMEM and PV
+// issue, 14 positions, scales and L2 prefetch, 15 pushes.
 // =============================================================================
 constexpr int kF8Heads = 64;           // heads of a CTA's QK and softmax
 constexpr int kF8Nt = 128;             // positions of a tile
 constexpr int kF8Block = kF8Nt * 128;  // 16 KB
-__host__ __device__ constexpr int f8_ring(bool pair) { return pair ? 4 : 2; }         // blocks that only QK reads
+__host__ __device__ constexpr int f8_ring(bool pair) { return pair ? 3 : 2; }         // blocks that only QK reads
 __host__ __device__ constexpr int f8_ring_per(bool pair) { return pair ? 3 : 1; }     // of them a tile
 __host__ __device__ constexpr int f8_stages(bool pair) { return pair ? 3 : 2; }       // stages of own columns
 __host__ __device__ constexpr int f8_own(bool pair) { return pair ? 2 : 4; }          // blocks of a stage
 __host__ __device__ constexpr int f8_own_at(bool pair, int st, int i) { return (f8_ring(pair) + f8_own(pair) * st + i) * kF8Block; }
-constexpr int kF8OffP = 10 * kF8Block;                       // hi limbs, then lo limbs
-constexpr int kF8OffQpe = kF8OffP + 2 * kF8Block;            // 128 rows (the lo rows are zero)
+// A limb of a CTA's P: 64 heads x 128 positions (K-major, 128-byte swizzle).
+constexpr int kF8Limb = kF8Nt * kF8Heads;
+// Where tile j's hi or lo limbs of P lie.  Pair: three buffers of 128 heads take
+// turns (two for each limb would cost a stage).  Single: two of both limbs.
+__host__ __device__ constexpr int f8_p_at(bool pair, int j, int lo) {
+  return f8_own_at(pair, f8_stages(pair), 0) + (pair ? (2 * j + lo) % 3 * (2 * kF8Limb) : (j & 1) * (2 * kF8Limb) + lo * kF8Limb);
+}
+constexpr int kF8OffQpe = 12 * kF8Block;                     // 128 rows (the lo rows are zero)
 constexpr int kF8OffKey = kF8OffQpe + kF8Block;              // f32 [4][3][128]: what a position's scale enters by
 constexpr int kF8OffPos = kF8OffKey + 4 * 3 * kF8Nt * 4;     // int [4][128]: a tile's positions, -1 = masked
 constexpr int kF8OffRed = kF8OffPos + 4 * kF8Nt * 4;         // f32 [2][2][64]
@@ -141,8 +146,8 @@ constexpr int kF8OffFin = kF8OffMove + 2 * 2 * 272;          // f32 [128]: one o
 constexpr int kF8OffBar = kF8OffFin + kH * 4;
 constexpr int kF8SmemBytes = kF8OffBar + 512 + kSmemAlignPad;
 constexpr int kF8SoftmaxWarps = 8;
-constexpr int kF8GatherWarp = 8, kF8GatherWarps = 4, kF8QkWarp = 12, kF8PvWarp = 13, kF8IndexWarp = 14;
-constexpr int kF8Threads = 480;
+constexpr int kF8GatherWarp = 8, kF8GatherWarps = 4, kF8QkWarp = 12, kF8PvWarp = 13, kF8IndexWarp = 14, kF8PushWarp = 15;
+constexpr int kF8Threads = 512;
 constexpr uint32_t kF8ColS = 0;    // scores: 128 columns
 constexpr uint32_t kF8ColQ = 128;  // the query's limbs: 128 columns of four codes
 constexpr uint32_t kF8ColO = 256;  // pair: 2 blocks of 128 heads; single: 4 blocks of 64
@@ -162,28 +167,28 @@ struct F8Move {
   uint32_t moved[4];       // the heads whose factor is not 1, 16 a word
 };
 static_assert(sizeof(F8Move) == 272, "kF8OffFin");
-// A limb of a CTA's P: 64 heads x 128 positions (K-major, 128-byte swizzle).  A
-// CTA of a pair sends its peer both limbs and its F8Move.
-constexpr int kF8Limb = kF8Nt * kF8Heads;
 static_assert(kF8SmemBytes <= 232448, "shared memory");
 static_assert(4 * kF8GatherWarps % 8 == 0, "a gather warp's rows share their swizzle");
-static_assert(f8_ring(true) + f8_stages(true) * f8_own(true) == 10 && f8_ring(false) + f8_stages(false) * f8_own(false) == 10, "blocks");
+static_assert(f8_own_at(true, 3, 0) + 3 * kF8Block <= kF8OffQpe && f8_own_at(false, 2, 0) + 2 * kF8Block <= kF8OffQpe, "blocks");
 
 struct F8Bars {
   uint64_t q_tma;         // the query's boxes landed
   uint64_t q_full;        // 8 softmax warps: the query's limbs are in TMEM
   uint64_t ring_full[2];  // the gather lanes, once a block: the tile's ring blocks have landed
-  uint64_t ring_empty[4]; // MMA commit: QK has read it
+  uint64_t ring_empty[3]; // MMA commit: QK has read it
   uint64_t own_full[3];   // the same of its stage
   uint64_t own_empty[3];  // MMA commit: PV has read the stage
   uint64_t tile_full[4];  // a tile's positions and scales
   uint64_t tile_done[4];  // MMA commit: its PV is done
   uint64_t s_full;        // MMA commit: scores ready
   uint64_t s_empty;       // 8 softmax warps: scores read
-  uint64_t p_own;         // 8 softmax warps: the CTA's part of P written
-  uint64_t p_hi, p_lo;    // pair: one arming arrival and the peer's limb
+  uint64_t p_own[2];      // 8 softmax warps: the CTA's part of P written
+  uint64_t o_ready[2];    // the same: O rescaled
+  uint64_t p_hi[2], p_lo[2];  // pair: one arming arrival and the peer's limb
   uint64_t moves[2];      // pair: one arming arrival and the peer's F8Move
-  uint64_t p_free;        // MMA commit of the CTA's (pair: and the peer's) PV: P free, pushes gone, O stable
+  uint64_t hi_free;       // pair: MMA commit of both CTAs' PV of the hi limbs
+  uint64_t p_free[2];     // MMA commit of the CTA's (pair: and the peer's) PV: P free, pushes gone, O stable
+  uint64_t drained[2];    // the MMAs of an aborted kernel
   uint32_t tmem_addr;
   int abort_flag;
 };
@@ -209,7 +214,8 @@ sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __nv_bf
                          const int32_t* __restrict__ cache_slot, int n_slots, int n_heads, int* d_status) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = align_smem_1024(smem_raw);
-  constexpr int kRing = f8_ring(kPair), kRingPer = f8_ring_per(kPair), kStages8 = f8_stages(kPair), kOwn = f8_own(kPair);
+  constexpr int kRing = f8_ring(kPair), kRingPer = f8_ring_per(kPair), kOwn = f8_own(kPair);
+  constexpr int kStages = f8_stages(kPair);
   constexpr int kCols = kPair ? kH : kF8Heads;  // heads of O and P
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = kPair ? cluster_ctarank() : 0u, peer = rank ^ 1u;
@@ -244,7 +250,7 @@ sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __nv_bf
     mbar_init(smem_u32(&bars->q_full), kF8SoftmaxWarps);
     for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&bars->ring_full[i]), 32 * kF8GatherWarps * kRingPer);
     for (int i = 0; i < kRing; ++i) mbar_init(smem_u32(&bars->ring_empty[i]), 1);
-    for (int s = 0; s < kStages8; ++s) {
+    for (int s = 0; s < kStages; ++s) {
       mbar_init(smem_u32(&bars->own_full[s]), 32 * kF8GatherWarps * kOwn);
       mbar_init(smem_u32(&bars->own_empty[s]), 1);
     }
@@ -253,17 +259,22 @@ sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __nv_bf
       mbar_init(smem_u32(&bars->tile_done[s]), 1);
     }
     mbar_init(smem_u32(&bars->s_full), 1);
+    mbar_init(smem_u32(&bars->hi_free), 2);
     mbar_init(smem_u32(&bars->s_empty), kF8SoftmaxWarps);
-    mbar_init(smem_u32(&bars->p_own), kF8SoftmaxWarps);
-    mbar_init(smem_u32(&bars->p_hi), 1);
-    mbar_init(smem_u32(&bars->p_lo), 1);
-    for (int s = 0; s < 2; ++s) mbar_init(smem_u32(&bars->moves[s]), 1);
-    if (kPair) {  // armed for the first tiles
-      mbar_arrive_expect_tx(smem_u32(&bars->p_hi), kF8Limb);
-      mbar_arrive_expect_tx(smem_u32(&bars->p_lo), kF8Limb);
-      for (int s = 0; s < 2; ++s) mbar_arrive_expect_tx(smem_u32(&bars->moves[s]), sizeof(F8Move));
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(smem_u32(&bars->drained[s]), 1);
+      mbar_init(smem_u32(&bars->p_own[s]), kF8SoftmaxWarps);
+      mbar_init(smem_u32(&bars->o_ready[s]), kF8SoftmaxWarps);
+      mbar_init(smem_u32(&bars->p_hi[s]), 1);
+      mbar_init(smem_u32(&bars->p_lo[s]), 1);
+      mbar_init(smem_u32(&bars->moves[s]), 1);
+      mbar_init(smem_u32(&bars->p_free[s]), kPair ? 2 : 1);
+      if (kPair) {  // armed for the first tiles
+        mbar_arrive_expect_tx(smem_u32(&bars->p_hi[s]), kF8Limb);
+        mbar_arrive_expect_tx(smem_u32(&bars->p_lo[s]), kF8Limb);
+        mbar_arrive_expect_tx(smem_u32(&bars->moves[s]), sizeof(F8Move));
+      }
     }
-    mbar_init(smem_u32(&bars->p_free), kPair ? 2 : 1);
     fence_mbarrier_init_cluster();
   }
   if (warp == kF8PvWarp) {
@@ -355,8 +366,9 @@ sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __nv_bf
     // A copy instruction brings 128 bytes of four positions; the warps
     // share a block's 32 of them, each with its positions in registers for all
     // five blocks (read for each copy, the copies issued at half the rate).
-    // Nothing here waits for a copy: the barriers complete when the data
-    // lands.
+    // Nothing here waits for a copy: the barriers complete when the data lands
+    // (with warps that wait for it and report it, 56.4 us instead of 53.3 at 64
+    // rows of 2048: a report needs a proxy fence, and waits behind the issue).
     const int g = warp - kF8GatherWarp;
     constexpr int kCopies = 32 / kF8GatherWarps;
     int rs = 0, st = 0;          // ring slot, stage
@@ -364,17 +376,17 @@ sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __nv_bf
     const uint32_t dst0 = s0 + sw128_offset(4 * g + (lane >> 3), lane & 7);
     for (int j = 0; j < n_tiles; ++j) {
       int pos[kCopies];
-      wait(smem_u32(&bars->tile_full[j & 3]), (j >> 2) & 1, ab);
+      const bool known = wait(smem_u32(&bars->tile_full[j & 3]), (j >> 2) & 1, ab);  // else timed out: nothing is read
 #pragma unroll
-      for (int i = 0; i < kCopies; ++i) pos[i] = pos_s[(j & 3) * kF8Nt + 4 * (g + kF8GatherWarps * i) + (lane >> 3)];
+      for (int i = 0; i < kCopies; ++i) pos[i] = known ? pos_s[(j & 3) * kF8Nt + 4 * (g + kF8GatherWarps * i) + (lane >> 3)] : -1;
       // the rotary rows, then 128 columns at a time: the peer's, the CTA's own
       // (one body for all: the warps of an SM fetch more code than its
       // instruction cache likes)
 #pragma unroll 1
       for (int i = 0; i < 5; ++i) {
         const bool ring = i < kRingPer;
-        uint64_t* full;
         uint32_t dst;
+        uint64_t* full;
         if (ring) {
           wait(smem_u32(&bars->ring_empty[rs]), rph, ab);
           full = &bars->ring_full[j & 1];
@@ -397,7 +409,7 @@ sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __nv_bf
         }
         cp_async_arrive(smem_u32(full));
       }
-      if (++st == kStages8) st = 0, sph ^= 1;
+      if (++st == kStages) st = 0, sph ^= 1;
     }
   } else if (warp == kF8QkWarp) {
     // ------------------------------------------------ query load, QK issue
@@ -447,64 +459,75 @@ sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __nv_bf
 #pragma unroll 1
         for (int i = 0; i < kOwn; ++i)
           qk(d_0 + (uint64_t)((f8_own_at(kPair, 0, 0) + (st * kOwn + i) * kF8Block) >> 4), lat(i));
-        if (++st == kStages8) st = 0, sph ^= 1;
+        if (++st == kStages) st = 0, sph ^= 1;
         mma_commit(smem_u32(&bars->s_full));
+      }
+      if (*ab.flag) drain_mmas(smem_u32(&bars->drained[0]));
+    }
+    __syncwarp();
+  } else if (warp == kF8PushWarp) {
+    // ------------------------------------------------ pushes
+    if (kPair && lane == 0) {
+      for (int j = 0; j < n_tiles; ++j) {
+        const int pb = j & 1;
+        if (!wait(smem_u32(&bars->p_own[pb]), (j >> 1) & 1, ab)) break;
+        // The peer's buffers are free: p_free and hi_free, which the softmax
+        // warps waited for, count its PVs too.
+        const uint32_t hi = s0 + f8_p_at(true, j, 0) + rank * kF8Limb, lo = s0 + f8_p_at(true, j, 1) + rank * kF8Limb;
+        bulk_push(cluster_map(hi, peer), hi, kF8Limb, cluster_map(smem_u32(&bars->p_hi[pb]), peer));
+        bulk_push(cluster_map(lo, peer), lo, kF8Limb, cluster_map(smem_u32(&bars->p_lo[pb]), peer));
       }
     }
     __syncwarp();
   } else if (warp == kF8PvWarp) {
-    // ------------------------------------------------ pushes, PV issue
+    // ------------------------------------------------ PV issue
     if (lane == 0) {
       constexpr uint32_t id_pv = idesc_e4m3_f32(128, kCols, true, false);
       const uint64_t d_0 = smem_desc_sw128(s0, 16, 1024);
-      const uint64_t p0 = d_0 + (uint64_t)(kF8OffP >> 4);
-      constexpr uint32_t kLoAt = (kPair ? 2 : 1) * kF8Limb;
-      const uint32_t src = s0 + kF8OffP + rank * kF8Limb, far = cluster_map(src, peer);
-      const uint32_t b_hi = cluster_map(smem_u32(&bars->p_hi), peer), b_lo = cluster_map(smem_u32(&bars->p_lo), peer);
       int st = 0;
       for (int j = 0; j < n_tiles; ++j) {
-        const uint32_t ph = j & 1;
-        wait(smem_u32(&bars->p_own), ph, ab);
+        const int pb = j & 1;
+        const uint32_t ph = (j >> 1) & 1;
+        wait(smem_u32(&bars->o_ready[pb]), ph, ab);  // P is written before that
         if (kPair) {
-          // The peer's P is free: p_free(j - 1), which the softmax warps
-          // waited for, counts its PV too.
-          bulk_push(far, src, kF8Limb, b_hi);
-          bulk_push(far + kLoAt, src + kLoAt, kF8Limb, b_lo);
-          wait_cluster(smem_u32(&bars->p_hi), ph, ab);
-          if (j + 1 < n_tiles) mbar_arrive_expect_tx(smem_u32(&bars->p_hi), kF8Limb);
+          if (wait_cluster(smem_u32(&bars->p_hi[pb]), ph, ab) && j + 2 < n_tiles)
+            mbar_arrive_expect_tx(smem_u32(&bars->p_hi[pb]), kF8Limb);
         }
         tc_fence_after();
         // 128 latent columns x the heads, 32 positions a step, hi limbs and
         // lo limbs.  Pair: all hi limbs first, the peer's lo limbs are still
         // on their way.
         const uint64_t v0 = d_0 + (uint64_t)((f8_own_at(kPair, 0, 0) + st * (kOwn * kF8Block)) >> 4);
-        auto pv = [&](int m, int k, int lo, bool first) {
-          mma_f8_ss(tmem + kF8ColO + m * kCols, v0 + (uint64_t)((m * kF8Block + k * 32 * 128) >> 4),
-                    p0 + (uint64_t)((lo * kLoAt + k * 32) >> 4), id_pv, first ? 0u : 1u);
+        const uint64_t p_hi = d_0 + (uint64_t)(f8_p_at(kPair, j, 0) >> 4), p_lo = d_0 + (uint64_t)(f8_p_at(kPair, j, 1) >> 4);
+        auto pv = [&](int m, int k, uint64_t p, bool first) {
+          mma_f8_ss(tmem + kF8ColO + m * kCols, v0 + (uint64_t)((m * kF8Block + k * 32 * 128) >> 4), p + (uint64_t)((k * 32) >> 4),
+                    id_pv, first ? 0u : 1u);
         };
         if (kPair) {
 #pragma unroll 1
           for (int m = 0; m < kOwn; ++m)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) pv(m, k, 0, j == 0 && k == 0);
-          wait_cluster(smem_u32(&bars->p_lo), ph, ab);
-          if (j + 1 < n_tiles) mbar_arrive_expect_tx(smem_u32(&bars->p_lo), kF8Limb);
+            for (int k = 0; k < 4; ++k) pv(m, k, p_hi, j == 0 && k == 0);
+          mma_commit_to(smem_u32(&bars->hi_free), (uint16_t)3);
+          if (wait_cluster(smem_u32(&bars->p_lo[pb]), ph, ab) && j + 2 < n_tiles)
+            mbar_arrive_expect_tx(smem_u32(&bars->p_lo[pb]), kF8Limb);
         }
 #pragma unroll 1
         for (int m = 0; m < kOwn; ++m)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            if (!kPair) pv(m, k, 0, j == 0 && k == 0);
-            pv(m, k, 1, false);
+            if (!kPair) pv(m, k, p_hi, j == 0 && k == 0);
+            pv(m, k, p_lo, false);
           }
         mma_commit(smem_u32(&bars->own_empty[st]));
         mma_commit(smem_u32(&bars->tile_done[j & 3]));
         if (kPair)
-          mma_commit_to(smem_u32(&bars->p_free), (uint16_t)3);
+          mma_commit_to(smem_u32(&bars->p_free[pb]), (uint16_t)3);
         else
-          mma_commit(smem_u32(&bars->p_free));
-        if (++st == kStages8) st = 0;
+          mma_commit(smem_u32(&bars->p_free[pb]));
+        if (++st == kStages) st = 0;
       }
+      if (*ab.flag) drain_mmas(smem_u32(&bars->drained[1]));
     }
     __syncwarp();
   } else {
@@ -591,7 +614,7 @@ sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __nv_bf
     float m_ref = kF8NoRef, l = 0.f;
     for (int j = 0; j < n_tiles; ++j) {
       const ulonglong2* kt = reinterpret_cast<const ulonglong2*>(key + (j & 3) * (3 * kF8Nt) + first);
-      F8Move* mv = moves + 2 * (j & 1) + rank;  // tile j - 2's is done: P(j - 1) came after its PVs
+      F8Move* mv = moves + 2 * (j & 1) + rank;  // tile j - 2's is done: its PVs are
       uint64_t y[16];  // pairs of positions
       wait(smem_u32(&bars->s_full), j & 1, ab);
       tc_fence_after();
@@ -671,20 +694,34 @@ sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __nv_bf
       const float2 l01 = unpack_f32x2(add_f32x2(l2[0], l2[1]));
       l += l01.x + l01.y;
 
+      if (j >= 2) wait_cluster(smem_u32(&bars->p_free[j & 1]), ((j >> 1) - 1) & 1, ab);  // tile j - 2's lo limbs lay where the hi limbs go
+      const uint32_t hi_at = s0 + f8_p_at(kPair, j, 0) + rank * kF8Limb, lo_at = s0 + f8_p_at(kPair, j, 1) + rank * kF8Limb;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        st_shared_v4(hi_at + sw128_offset(hd, (first >> 4) + u), p_hi[4 * u], p_hi[4 * u + 1], p_hi[4 * u + 2], p_hi[4 * u + 3]);
+      // the lo limbs go where tile j - 1's hi limbs lay
+      if (kPair && j >= 1) wait_cluster(smem_u32(&bars->hi_free), (j - 1) & 1, ab);
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        st_shared_v4(lo_at + sw128_offset(hd, (first >> 4) + u), p_lo[4 * u], p_lo[4 * u + 1], p_lo[4 * u + 2], p_lo[4 * u + 3]);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars->p_own[j & 1]));
+
       // The heads of either CTA that moved: their columns of this CTA's O,
       // between PV(j - 1) and PV(j); 16 columns that hold none of them are left
       // alone.  The CTA's own words come from its other warps.
       if (kPair) {
-        wait_cluster(smem_u32(&bars->moves[j & 1]), (j >> 1) & 1, ab);
-        if (tid == 0 && j + 2 < n_tiles) mbar_arrive_expect_tx(smem_u32(&bars->moves[j & 1]), sizeof(F8Move));
+        if (wait_cluster(smem_u32(&bars->moves[j & 1]), (j >> 1) & 1, ab) && tid == 0 && j + 2 < n_tiles)
+          mbar_arrive_expect_tx(smem_u32(&bars->moves[j & 1]), sizeof(F8Move));
       }
       named_bar_sync(1, kSoftmaxThreads);
       if (j > 0) {
-        wait_cluster(smem_u32(&bars->p_free), (j - 1) & 1, ab);  // the one P buffer; O is stable
         const F8Move* both = moves + 2 * (j & 1);
         const uint4 w0 = *reinterpret_cast<const uint4*>(both[0].moved);
         const uint4 w1 = kPair ? *reinterpret_cast<const uint4*>(both[1].moved) : make_uint4(0, 0, 0, 0);
         if ((w0.x | w0.y | w0.z | w0.w | w1.x | w1.y | w1.z | w1.w) != 0) {
+          wait_cluster(smem_u32(&bars->p_free[(j - 1) & 1]), ((j - 1) >> 1) & 1, ab);  // PV(j - 1) is done
           tc_fence_after();
 #pragma unroll 1
           for (int cc = 0; cc < 8; ++cc) {
@@ -710,15 +747,8 @@ sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __nv_bf
           tc_fence_before();
         }
       }
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const uint32_t dst = s0 + kF8OffP + rank * kF8Limb + sw128_offset(hd, (first >> 4) + u);
-        st_shared_v4(dst, p_hi[4 * u], p_hi[4 * u + 1], p_hi[4 * u + 2], p_hi[4 * u + 3]);
-        st_shared_v4(dst + (kPair ? 2 : 1) * kF8Limb, p_lo[4 * u], p_lo[4 * u + 1], p_lo[4 * u + 2], p_lo[4 * u + 3]);
-      }
-      fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars->p_own));
+      if (lane == 0) mbar_arrive(smem_u32(&bars->o_ready[j & 1]));
     }
 
     // The row sums over the positions; what normalises O goes to the peer too.
@@ -736,21 +766,22 @@ sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __nv_bf
         lse_part[((size_t)b * n_split + split) * n_heads + h0 + hd] =
             sum == 0.f ? -INFINITY : (m_ref + log2f(sum)) * 0.6931471805599453f;
     }
-    wait_cluster(smem_u32(&bars->p_free), (n_tiles - 1) & 1, ab);
+    // the last PV ends after all others
+    wait_cluster(smem_u32(&bars->p_free[(n_tiles - 1) & 1]), ((n_tiles - 1) >> 1) & 1, ab);
     tc_fence_after();
   }
 
   // Both CTAs' sums are in place, and neither touches the other's memory again
-  // (after a timed-out wait, pushes and arrivals may still be on their way).
-  if (kPair) {
-    if (*ab.flag) {
-      const uint64_t t0 = global_timer_ns();
-      while (global_timer_ns() - t0 < 2000000ull) {
-      }
+  // (after a timed-out wait, pushes, copies and arrivals may still be on their
+  // way).
+  cp_async_wait_all();
+  if (*ab.flag) {
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 2000000ull) {
     }
-    __syncwarp();
-    cluster_sync();
   }
+  __syncwarp();
+  if (kPair) cluster_sync();
   __syncthreads();
 
   if (warp < kF8SoftmaxWarps) {

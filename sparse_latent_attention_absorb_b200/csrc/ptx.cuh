@@ -104,6 +104,19 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+// Whether the phase has completed, without waiting for it.
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Cluster-scope acquire: for barriers whose arrivals come from the peer CTA.
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
   uint32_t ok;
@@ -367,6 +380,16 @@ __device__ __forceinline__ void mma_commit_to(uint32_t bar, uint16_t cta_mask) {
       "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
       "h"(cta_mask)
       : "memory");
+}
+
+// On the way out of an aborted kernel: until this thread's MMAs in flight have
+// completed (`bar`: a barrier of one arrival that nothing else uses), for 10 ms
+// at most.
+static __device__ __noinline__ void drain_mmas(uint32_t bar) {
+  mma_commit(bar);
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_test_wait(bar, 0) && global_timer_ns() - t0 < 10000000ull) {
+  }
 }
 
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }

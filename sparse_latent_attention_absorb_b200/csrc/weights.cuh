@@ -72,6 +72,7 @@ struct WtBars {
   uint64_t full[4], empty[4];            // groups
   uint64_t tile_full[4], tile_done[4];   // positions and scales written, used up
   uint64_t s_full[2], s_empty[2];
+  uint64_t drained;                      // the MMAs of an aborted kernel
   uint32_t tmem_addr;
   int abort_flag;
 };
@@ -115,6 +116,7 @@ accumulate_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __nv_b
       mbar_init(smem_u32(&bars->tile_full[i]), 1);
       mbar_init(smem_u32(&bars->tile_done[i]), 4);
     }
+    mbar_init(smem_u32(&bars->drained), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&bars->s_full[i]), 1);
       mbar_init(smem_u32(&bars->s_empty[i]), 8);
@@ -197,9 +199,9 @@ accumulate_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __nv_b
     wait(smem_u32(&bars->q_full), 0, ab);  // the query's boxes lie in the ring until they are in TMEM
     for (int j = 0; j < n_tiles; ++j) {
       int pos[kCopies];
-      wait(smem_u32(&bars->tile_full[j & 3]), (j >> 2) & 1, ab);
+      const bool known = wait(smem_u32(&bars->tile_full[j & 3]), (j >> 2) & 1, ab);  // else timed out: nothing is read
 #pragma unroll
-      for (int u = 0; u < kCopies; ++u) pos[u] = pos_s[(j & 3) * kWtNt + 4 * (g + kWtGatherWarps * u) + (lane >> 3)];
+      for (int u = 0; u < kCopies; ++u) pos[u] = !known ? -1 : pos_s[(j & 3) * kWtNt + 4 * (g + kWtGatherWarps * u) + (lane >> 3)];
 #pragma unroll 1
       for (int i = 0; i < kBlocks; ++i) {
         if (i % kGroup == 0) wait(smem_u32(&bars->empty[gr]), ph, ab);
@@ -261,6 +263,7 @@ accumulate_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __nv_b
         }
         mma_commit(smem_u32(&bars->s_full[j & 1]));
       }
+      if (*ab.flag) drain_mmas(smem_u32(&bars->drained));
     }
     __syncwarp();
   } else if (warp < 8) {
@@ -343,7 +346,7 @@ accumulate_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __nv_b
     for (int j = 0; j < n_tiles; ++j) {
       float* rt = red + (j & 1) * (4 * kWtNt) + qd * kWtNt + 64 * ch;
       const ulonglong2* kt = reinterpret_cast<const ulonglong2*>(sc + (j & 3) * kWtNt + 64 * ch);
-      wait(smem_u32(&bars->tile_full[j & 3]), (j >> 2) & 1, ab);
+      const bool known = wait(smem_u32(&bars->tile_full[j & 3]), (j >> 2) & 1, ab);  // else timed out: nothing is added
       wait(smem_u32(&bars->s_full[j & 1]), (j >> 1) & 1, ab);
       tc_fence_after();
 #pragma unroll 1
@@ -377,13 +380,14 @@ accumulate_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __nv_b
         const float* s4 = red + (j & 1) * (4 * kWtNt) + tid;
         const int pos = pos_s[(j & 3) * kWtNt + tid];
         // distinct positions: an addition a position, in whatever order
-        if (pos >= 0) atomicAdd(acc + (size_t)b * S_max + pos, (s4[0] + s4[kWtNt]) + (s4[2 * kWtNt] + s4[3 * kWtNt]));
+        if (known && pos >= 0) atomicAdd(acc + (size_t)b * S_max + pos, (s4[0] + s4[kWtNt]) + (s4[2 * kWtNt] + s4[3 * kWtNt]));
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars->tile_done[j & 3]));
       }
     }
   }
 
+  cp_async_wait_all();  // after a timed-out wait, copies may still be in flight
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
