@@ -38,10 +38,10 @@ __device__ __forceinline__ __half2 limb_rest(uint32_t f16x2, uint32_t first) {
   const uint32_t cut = first & 0xbf80bf80u;
   return __hsub2(*reinterpret_cast<const __half2*>(&f16x2), *reinterpret_cast<const __half2*>(&cut));
 }
-// The E4M3 bytes of four rounded fp16 numbers (sign, then bits 13..7 of each).
+// The E4M3 bytes of four rounded fp16 numbers (sign, then bits 13..7 of each:
+// the magnitude, below 2^14, is doubled under the sign).
 __device__ __forceinline__ uint32_t limb_bytes(uint32_t a, uint32_t b) {
-  const uint32_t u = (a & 0x80008000u) | ((a << 1) & 0x7f007f00u), v = (b & 0x80008000u) | ((b << 1) & 0x7f007f00u);
-  return __byte_perm(u, v, 0x7531);
+  return __byte_perm(a + (a & 0x7fff7fffu), b + (b & 0x7fff7fffu), 0x7531);
 }
 __device__ __forceinline__ uint32_t limb_bytes_positive(uint32_t a, uint32_t b) {
   return __byte_perm(a << 1, b << 1, 0x7531);
@@ -188,6 +188,7 @@ struct F8Bars {
   uint64_t moves[2];      // pair: one arming arrival and the peer's F8Move
   uint64_t hi_free;       // pair: MMA commit of both CTAs' PV of the hi limbs
   uint64_t p_free[2];     // MMA commit of the CTA's (pair: and the peer's) PV: P free, pushes gone, O stable
+  uint64_t fin_full;      // pair: one arming arrival and the peer's half of fin
   uint64_t drained[2];    // the MMAs of an aborted kernel
   uint32_t tmem_addr;
   int abort_flag;
@@ -244,38 +245,46 @@ sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __nv_bf
   F8Bars* bars = reinterpret_cast<F8Bars*>(smem + kF8OffBar);
   const AbortState ab{&bars->abort_flag, d_status};
 
-  if (tid == 0) {
-    bars->abort_flag = 0;
-    mbar_init(smem_u32(&bars->q_tma), 1);
-    mbar_init(smem_u32(&bars->q_full), kF8SoftmaxWarps);
-    for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&bars->ring_full[i]), 32 * kF8GatherWarps * kRingPer);
-    for (int i = 0; i < kRing; ++i) mbar_init(smem_u32(&bars->ring_empty[i]), 1);
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(smem_u32(&bars->own_full[s]), 32 * kF8GatherWarps * kOwn);
-      mbar_init(smem_u32(&bars->own_empty[s]), 1);
-    }
-    for (int s = 0; s < 4; ++s) {
-      mbar_init(smem_u32(&bars->tile_full[s]), 1);
-      mbar_init(smem_u32(&bars->tile_done[s]), 1);
-    }
-    mbar_init(smem_u32(&bars->s_full), 1);
-    mbar_init(smem_u32(&bars->hi_free), 2);
-    mbar_init(smem_u32(&bars->s_empty), kF8SoftmaxWarps);
-    for (int s = 0; s < 2; ++s) {
+  if (warp == kF8QkWarp) {
+    // (the lanes share the barriers: one thread took a microsecond)
+    if (lane == 0) {
+      bars->abort_flag = 0;
+      mbar_init(smem_u32(&bars->q_tma), 1);
+      mbar_init(smem_u32(&bars->q_full), kF8SoftmaxWarps);
+      mbar_init(smem_u32(&bars->s_full), 1);
+      mbar_init(smem_u32(&bars->s_empty), kF8SoftmaxWarps);
+      mbar_init(smem_u32(&bars->hi_free), 2);
+      mbar_init(smem_u32(&bars->fin_full), 1);
+      if (kPair) mbar_arrive_expect_tx(smem_u32(&bars->fin_full), kF8Heads * 4);
+    } else if (lane < 3) {
+      const int s = lane - 1;
+      mbar_init(smem_u32(&bars->ring_full[s]), 32 * kF8GatherWarps * kRingPer);
       mbar_init(smem_u32(&bars->drained[s]), 1);
       mbar_init(smem_u32(&bars->p_own[s]), kF8SoftmaxWarps);
       mbar_init(smem_u32(&bars->o_ready[s]), kF8SoftmaxWarps);
+      mbar_init(smem_u32(&bars->p_free[s]), kPair ? 2 : 1);
+    } else if (lane < 5) {
+      const int s = lane - 3;
       mbar_init(smem_u32(&bars->p_hi[s]), 1);
       mbar_init(smem_u32(&bars->p_lo[s]), 1);
       mbar_init(smem_u32(&bars->moves[s]), 1);
-      mbar_init(smem_u32(&bars->p_free[s]), kPair ? 2 : 1);
       if (kPair) {  // armed for the first tiles
         mbar_arrive_expect_tx(smem_u32(&bars->p_hi[s]), kF8Limb);
         mbar_arrive_expect_tx(smem_u32(&bars->p_lo[s]), kF8Limb);
         mbar_arrive_expect_tx(smem_u32(&bars->moves[s]), sizeof(F8Move));
       }
+    } else if (lane < 9) {
+      const int s = lane - 5;
+      mbar_init(smem_u32(&bars->tile_full[s]), 1);
+      mbar_init(smem_u32(&bars->tile_done[s]), 1);
+      if (s < kRing) mbar_init(smem_u32(&bars->ring_empty[s]), 1);
+      if (s < kStages) {
+        mbar_init(smem_u32(&bars->own_full[s]), 32 * kF8GatherWarps * kOwn);
+        mbar_init(smem_u32(&bars->own_empty[s]), 1);
+      }
     }
     fence_mbarrier_init_cluster();
+    __syncwarp();
   }
   if (warp == kF8PvWarp) {
     tmem_alloc(smem_u32(&bars->tmem_addr), 512);
@@ -575,21 +584,6 @@ sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __nv_bf
       const int e = limb_exponent(am);
       const float mul = exp2_int(e);
       c2 = scale * 1.4426950408889634f * exp2_int(-e);
-#pragma unroll 2
-      for (int c = 0; c < 16; ++c) {  // 16 columns: of two pieces, each row of the head converts one
-        const uint4 v = piece(2 * c + (hi_row ? 0 : 1));
-        uint32_t r[4];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          uint32_t hi, lo;
-          limbs4(u ? v.z : v.x, u ? v.w : v.y, mul * (1.f / 256.f), 1.f / kLimbLo, &hi, &lo);
-          const uint32_t other = __shfl_xor_sync(0xffffffffu, hi_row ? lo : hi, 16);
-          r[u] = hi_row ? hi : other;
-          r[2 + u] = hi_row ? other : lo;
-        }
-        tmem_st4(tmem + lane_base + kF8ColQ + 64 * ch + 4 * c, r);
-      }
-      tmem_wait_st();
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const uint32_t w[4] = {r4[u].x, r4[u].y, r4[u].z, r4[u].w};
@@ -600,6 +594,34 @@ sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __nv_bf
         st_shared_v4(s0 + kF8OffQpe + sw128_offset(32 * qd + lane, 4 * ch + u), o[0], o[1], o[2], o[3]);
       }
       fence_proxy_async_smem();
+      // 64 columns at a time: of two pieces of eight, each row of the head
+      // converts one.  The loads go first, so that their latency is met once.
+#pragma unroll 1
+      for (int c4 = 0; c4 < 4; ++c4) {
+        uint4 v[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = piece(8 * c4 + 2 * q + (hi_row ? 0 : 1));
+        uint32_t keep[8], send[8], r[16];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            uint32_t hi, lo;
+            limbs4(u ? v[q].z : v[q].x, u ? v[q].w : v[q].y, mul * (1.f / 256.f), 1.f / kLimbLo, &hi, &lo);
+            keep[2 * q + u] = hi_row ? hi : lo;
+            send[2 * q + u] = hi_row ? lo : hi;
+          }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, send[2 * q + u], 16);
+            r[4 * q + u] = hi_row ? keep[2 * q + u] : other;
+            r[4 * q + 2 + u] = hi_row ? other : keep[2 * q + u];
+          }
+        tmem_st16(tmem + lane_base + kF8ColQ + 64 * ch + 16 * c4, r);
+      }
+      tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars->q_full));
@@ -761,7 +783,7 @@ sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __nv_bf
       const float inv = sum == 0.f ? 0.f : (1.f / 256.f) / sum;  // P's E4M3 value is 2^8 times its fp16 one
       fin[h0 + hd] = inv;
       if (kPair)
-        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_map(smem_u32(&fin[h0 + hd]), peer)), "f"(inv) : "memory");
+        st_async_b32(cluster_map(smem_u32(&fin[h0 + hd]), peer), __float_as_uint(inv), cluster_map(smem_u32(&bars->fin_full), peer));
       if (hd < live)
         lse_part[((size_t)b * n_split + split) * n_heads + h0 + hd] =
             sum == 0.f ? -INFINITY : (m_ref + log2f(sum)) * 0.6931471805599453f;
@@ -771,9 +793,8 @@ sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __nv_bf
     tc_fence_after();
   }
 
-  // Both CTAs' sums are in place, and neither touches the other's memory again
-  // (after a timed-out wait, pushes, copies and arrivals may still be on their
-  // way).
+  // A CTA that gave up waiting leaves nothing on its way into its own or its
+  // peer's memory.
   cp_async_wait_all();
   if (*ab.flag) {
     const uint64_t t0 = global_timer_ns();
@@ -781,27 +802,21 @@ sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __nv_bf
     }
   }
   __syncwarp();
-  if (kPair) cluster_sync();
-  __syncthreads();
+  if (kPair) cluster_arrive();  // from here on nothing of the peer's is touched
 
   if (warp < kF8SoftmaxWarps) {
-    // O normalised and turned round through the idle blocks (a head's columns
-    // contiguous), one bulk copy a head.
+    // O normalised: of two heads, an even lane takes the first and its
+    // neighbour the second, two latent columns in one word.  A warp writes 64
+    // bytes of each of two heads at a time.
+    named_bar_sync(1, kSoftmaxThreads);
+    if (kPair) wait_cluster(smem_u32(&bars->fin_full), 0, ab);
     const uint32_t lane_base = (uint32_t)(qd * 32) << 16;
-    constexpr int kWidth = kOwn * 128;
-    constexpr uint32_t kRow = kWidth * 2 + 64;  // rows of two heads fall on the two halves of the banks
-#pragma unroll 1
-    for (int cc = 0; cc < 8; ++cc) {
-      const int c0 = 128 * ch + 16 * cc, m = c0 / kCols, hb = c0 % kCols;
-      uint32_t ov[16];
-      tmem_ld16(tmem + lane_base + kF8ColO + c0, ov);
-      tmem_wait_ld();
-      // Of two heads, an even lane takes the first and its neighbour the
-      // second: two latent columns in one word.
-      const uint32_t dst = s0 + (uint32_t)(hb + (lane & 1)) * kRow + (uint32_t)(m * 128 + 32 * qd + (lane & ~1)) * 2u;
-      const float4* f4 = reinterpret_cast<const float4*>(fin + hb);
+    uint32_t* o_row = reinterpret_cast<uint32_t*>(o_part + ((size_t)b * n_split + split) * n_heads * kDl) + rank * 128 + 16 * qd + (lane >> 1);
+    auto write = [&](int cc, const uint32_t (&ov)[32]) {
+      const int c0 = 128 * ch + 32 * cc, m = c0 / kCols, hb = c0 % kCols + (lane & 1);
+      const float4* f4 = reinterpret_cast<const float4*>(fin + c0 % kCols);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 8; ++i) {
         const float4 f = f4[i];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
@@ -809,16 +824,22 @@ sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __nv_bf
           const float y = __uint_as_float(ov[4 * i + 2 * u + 1]) * (u ? f.w : f.y);
           const float other = __shfl_xor_sync(0xffffffffu, (lane & 1) ? x : y, 1);
           const uint32_t w = (lane & 1) ? pack_bf16x2(other, y) : pack_bf16x2(x, other);
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + (uint32_t)(4 * i + 2 * u) * kRow), "r"(w) : "memory");
+          const int head = hb + 4 * i + 2 * u;
+          if (head < n_heads) o_row[(uint32_t)head * (kDl / 2) + m * 64] = w;
         }
       }
-    }
-    fence_proxy_async_smem();
-    named_bar_sync(1, kSoftmaxThreads);
-    if (tid < kCols && tid < n_heads) {
-      bulk_store(o_part + (((size_t)b * n_split + split) * n_heads + tid) * kDl + rank * 256, s0 + tid * kRow, kWidth * 2);
-      bulk_commit();
-      bulk_wait_read();
+    };
+    const uint32_t o_at = tmem + lane_base + kF8ColO + 128 * ch;
+    uint32_t oa[32], ob[32];
+    tmem_ld32(o_at, oa);
+#pragma unroll 1
+    for (int cc = 0; cc < 4; cc += 2) {
+      tmem_wait_ld();
+      tmem_ld32(o_at + 32 * (cc + 1), ob);
+      write(cc, oa);
+      tmem_wait_ld();
+      if (cc == 0) tmem_ld32(o_at + 64, oa);
+      write(cc + 1, ob);
     }
   }
 
@@ -826,6 +847,7 @@ sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __nv_bf
   __syncthreads();
   tc_fence_after();
   if (warp == kF8PvWarp) tmem_dealloc(tmem, 512);
+  if (kPair) cluster_wait();  // the peer may still write to this CTA until then
 }
 
 }  // namespace mla
