@@ -32,15 +32,16 @@ __device__ __forceinline__ int scale_exponent(float amax) {
   return max(k - (m <= 0.875f ? 9 : 8), kMinScaleExp);
 }
 
-// The sequence of token i: how many of cu[1..n_seq] are at most i.  Every lane
+// How many of f(1) .. f(n_seq), which do not fall, are at most i.  Every lane
 // probes one point of the range that is left (log32 n_seq rounds of loads).
-__device__ __forceinline__ int sequence_of(const int32_t* cu, int n_seq, int i, int lane) {
+template <typename F>
+__device__ __forceinline__ int count_at_most(F f, int n_seq, int i, int lane) {
   int lo = 0, hi = n_seq;  // the answer lies in [lo, hi]
   while (lo < hi) {
     const int step = (hi - lo + 31) / 32;
-    const int k = lo + (lane + 1) * step;  // cu[k] <= i: the answer is at least k
-    const uint32_t yes = __ballot_sync(0xffffffffu, k <= hi && __ldg(cu + min(k, n_seq)) <= i);
-    const int n = __popc(yes);             // cu does not fall: a prefix of the lanes
+    const int k = lo + (lane + 1) * step;  // f(k) <= i: the answer is at least k
+    const uint32_t yes = __ballot_sync(0xffffffffu, k <= hi && f(min(k, n_seq)) <= i);
+    const int n = __popc(yes);             // a prefix of the lanes
     lo += n * step;
     hi = min(hi, lo + step - 1);
   }
@@ -58,30 +59,6 @@ struct AppendArgs {
   float* kv_scale;
   int N, n_seq, S_max, n_slots, shift, n_blocks;
 };
-
-// Where token i goes: position (negative: nowhere), slot, its sequence's first
-// token, and how many tokens from i on share its block (the token's block
-// starts with it or at its sequence's first token, or it is not `leader`).
-struct AppendPlace {
-  int pos, slot, count;
-  bool leader;
-};
-__device__ __forceinline__ AppendPlace place_of(const AppendArgs& a, int i, int lane) {
-  AppendPlace p{-1, 0, 0, false};
-  const int seq = sequence_of(a.cu_rows, a.n_seq, i, lane);
-  if (seq >= a.n_seq) return p;  // behind the last sequence
-  const int first = __ldg(a.cu_rows + seq), next = __ldg(a.cu_rows + seq + 1);
-  const long long at = (long long)__ldg(a.start_pos + seq) + (i - first);
-  const int slot = a.cache_slot ? __ldg(a.cache_slot + seq) : seq;
-  if (i < first || at < 0 || at >= a.S_max || slot < 0 || slot >= a.n_slots) return p;
-  p.pos = (int)at;
-  p.slot = slot;
-  const int in_block = p.pos & ((1 << a.shift) - 1);
-  p.leader = in_block == 0 || i == first;
-  p.count = min(min((1 << a.shift) - in_block, min(next, a.N) - i), a.S_max - p.pos);
-  if (p.count < 1) p.pos = -1;  // cu_rows that falls
-  return p;
-}
 
 // A warp's lane holds columns 8 lane.. and 256 + 8 lane.. of a latent row.
 struct LatentRow {
@@ -161,63 +138,87 @@ append_fp8_rows_kernel(const AppendArgs a) {
   if (i >= a.N) return;
   const LatentRow r = load_row(a.kv_new + (size_t)i * kDl, lane);  // in flight during the search
   const uint32_t pe2 = load_pe(a.pe_new + (size_t)i * kDr, lane);
-  const AppendPlace p = place_of(a, i, lane);
-  if (p.pos < 0) return;
+  const int seq = count_at_most([&](int q) { return __ldg(a.cu_rows + q); }, a.n_seq, i, lane);
+  if (seq >= a.n_seq) return;  // behind the last sequence
+  const int first = __ldg(a.cu_rows + seq);
+  const long long at = (long long)__ldg(a.start_pos + seq) + (i - first);
+  const int slot = a.cache_slot ? __ldg(a.cache_slot + seq) : seq;
+  if (i < first || at < 0 || at >= a.S_max || slot < 0 || slot >= a.n_slots) return;
   const int e = scale_exponent(row_amax(r));
-  store_row(a, p.slot, p.pos, r, pe2, exp2_int(-e), lane);
-  if (lane == 0) a.kv_scale[(size_t)p.slot * a.n_blocks + p.pos] = exp2_int(e);
+  store_row(a, slot, (int)at, r, pe2, exp2_int(-e), lane);
+  if (lane == 0) a.kv_scale[(size_t)slot * a.n_blocks + at] = exp2_int(e);
 }
 
-// Shared scales: a CTA looks at `per` tokens in a row and writes the blocks
-// that one of them leads, all warps at a block's rows.  (The rows are read
-// twice, the second time from L1 or L2.)
+// Shared scales: a CTA per block of positions, all warps at its rows, up to
+// kHold rows of a warp held in registers between the maximum and the rounding
+// (the others are read twice, the second time from L1 or L2).
+//
+// Sequence q's blocks are the CTAs from cu[q] / block + 2 q on: L tokens touch
+// at most L / block + 2 blocks, so they end before the next sequence's, and the
+// CTAs behind them return.
+constexpr int kHold = 4;
+__host__ __device__ inline int append_blocks_grid(int N, int n_seq, int shift) { return (N >> shift) + 2 * n_seq; }
+
 __global__ void __launch_bounds__(kAppendThreads)
-append_fp8_blocks_kernel(const AppendArgs a, int per) {
+append_fp8_blocks_kernel(const AppendArgs a) {
   constexpr int kWarps = kAppendThreads / 32;
-  __shared__ AppendPlace places[kWarps];
   __shared__ float tops[kWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int i0 = blockIdx.x * per;
-  if (warp < per) {
-    AppendPlace p{-1, 0, 0, false};
-    if (i0 + warp < a.N) p = place_of(a, i0 + warp, lane);
-    if (lane == 0) places[warp] = p;
-  }
-  __syncthreads();
-  for (int t = 0; t < per; ++t) {
-    const AppendPlace p = places[t];
-    if (p.pos < 0 || !p.leader) continue;
-    const __nv_bfloat16* kv = a.kv_new + (size_t)(i0 + t) * kDl;
-    const __nv_bfloat16* pe = a.pe_new + (size_t)(i0 + t) * kDr;
-    float* sp = a.kv_scale + (size_t)p.slot * a.n_blocks + (p.pos >> a.shift);
-    const int block0 = p.pos & ~((1 << a.shift) - 1), earlier = p.pos - block0;
-    const float old = earlier > 0 ? *sp : 0.f;
-    float top = 0.f;
-    for (int r = warp; r < p.count; r += kWarps) top = fmaxf(top, row_amax(load_row(kv + (size_t)r * kDl, lane)));
-    if (lane == 0) tops[warp] = top;
-    __syncthreads();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, at = (int)blockIdx.x;
+  auto first_cta = [&](int q) { return (min(max(__ldg(a.cu_rows + q), 0), a.N) >> a.shift) + 2 * q; };
+  const int seq = count_at_most(first_cta, a.n_seq, at, lane);
+  if (seq >= a.n_seq) return;
+  const int row0 = __ldg(a.cu_rows + seq), row1 = min(__ldg(a.cu_rows + seq + 1), a.N), start = __ldg(a.start_pos + seq);
+  const int slot = a.cache_slot ? __ldg(a.cache_slot + seq) : seq;
+  if (row0 < 0 || row0 >= row1 || slot < 0 || slot >= a.n_slots) return;
+  // positions [pos0, pos1) of the slot are written, this CTA's [p0, p1) in one block
+  const int pos0 = max(start, 0);
+  const int pos1 = (int)min((long long)start + (row1 - row0), (long long)a.S_max);
+  const long long block0 = (long long)((pos0 >> a.shift) + (at - first_cta(seq))) << a.shift;
+  if (block0 >= pos1) return;
+  const int p0 = max((int)block0, pos0), p1 = (int)min((long long)pos1, block0 + (1 << a.shift));
+  const int count = p1 - p0, earlier = p0 - (int)block0;
+  const __nv_bfloat16* kv = a.kv_new + ((long long)row0 + (p0 - (long long)start)) * kDl;
+  const __nv_bfloat16* pe = a.pe_new + ((long long)row0 + (p0 - (long long)start)) * kDr;
+  float* sp = a.kv_scale + (size_t)slot * a.n_blocks + (p0 >> a.shift);
+  LatentRow held[kHold];
+  uint32_t held_pe[kHold];
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, tops[w]);
-    const float need = exp2_int(scale_exponent(top));
-    const float s = fmaxf(need, old);
-    const float inv = 1.f / s;
-    if (earlier > 0 && s != old) {
-      const float ratio = old / s;
-      for (int r = warp; r < earlier; r += kWarps) {
-        const size_t at = (size_t)p.slot * a.S_max + block0 + r;
-        uint4* c = reinterpret_cast<uint4*>(a.kv8 + at * kDl) + lane;
-        uint32_t* q = reinterpret_cast<uint32_t*>(a.pe8 + at * kDr) + lane;
-        const uint4 codes = *c;
-        const uint32_t pe2 = *q;
-        *c = recode16(codes, ratio);
-        *q = rescale_pe(pe2, ratio);
-      }
-    }
-    for (int r = warp; r < p.count; r += kWarps)
-      store_row(a, p.slot, p.pos + r, load_row(kv + (size_t)r * kDl, lane), load_pe(pe + (size_t)r * kDr, lane), inv, lane);
-    __syncthreads();  // the scale is read before it is written, `tops` before the next block's
-    if (threadIdx.x == 0) *sp = s;
+  for (int u = 0; u < kHold; ++u) {
+    const int r = warp + u * kWarps;
+    held[u] = r < count ? load_row(kv + (size_t)r * kDl, lane) : LatentRow{};
+    held_pe[u] = r < count ? load_pe(pe + (size_t)r * kDr, lane) : 0u;
   }
+  const float old = earlier > 0 ? *sp : 0.f;
+  float top = 0.f;
+#pragma unroll
+  for (int u = 0; u < kHold; ++u) top = fmaxf(top, row_amax(held[u]));
+  for (int r = warp + kHold * kWarps; r < count; r += kWarps) top = fmaxf(top, row_amax(load_row(kv + (size_t)r * kDl, lane)));
+  if (lane == 0) tops[warp] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, tops[w]);
+  const float s = fmaxf(exp2_int(scale_exponent(top)), old);
+  const float inv = 1.f / s;
+  if (earlier > 0 && s != old) {
+    const float ratio = old / s;
+    for (int r = warp; r < earlier; r += kWarps) {
+      const size_t row = (size_t)slot * a.S_max + block0 + r;
+      uint4* c = reinterpret_cast<uint4*>(a.kv8 + row * kDl) + lane;
+      uint32_t* q = reinterpret_cast<uint32_t*>(a.pe8 + row * kDr) + lane;
+      const uint4 codes = *c;
+      const uint32_t pe2 = *q;
+      *c = recode16(codes, ratio);
+      *q = rescale_pe(pe2, ratio);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kHold; ++u) {
+    const int r = warp + u * kWarps;
+    if (r < count) store_row(a, slot, p0 + r, held[u], held_pe[u], inv, lane);
+  }
+  for (int r = warp + kHold * kWarps; r < count; r += kWarps)
+    store_row(a, slot, p0 + r, load_row(kv + (size_t)r * kDl, lane), load_pe(pe + (size_t)r * kDr, lane), inv, lane);
+  if (threadIdx.x == 0) *sp = s;  // (everyone has read it: the barrier)
 }
 
 }  // namespace mla

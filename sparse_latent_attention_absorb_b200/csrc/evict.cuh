@@ -69,6 +69,7 @@ evict_select_kernel(const float* acc, const int32_t* __restrict__ end_pos, float
   __shared__ int2 warp_sums[32];
   __shared__ uint32_t found[2];
   __shared__ int2 counts;
+  grid_dep_launch();  // the rows' kernel may come up
   const int n_cta = (int)cluster_size(), rank = (int)cluster_ctarank();
   const int b = blockIdx.x / n_cta, tid = threadIdx.x, lane = tid & 31;
   const float* w = acc + (size_t)b * S_max;
@@ -257,6 +258,7 @@ __global__ void __launch_bounds__(kMoveThreads, 1) evict_move_kernel(const MoveA
   constexpr size_t kRow = kVecs * 512;
   __shared__ float src_scale[kMoveRows], dst_scale[kMoveRows];
   const int b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  grid_dep_wait();  // kept and new_end come from the selection
   const int n = a.new_end[b];
   const int32_t* kept = a.kept + (size_t)b * a.keep;
   const size_t row0 = (size_t)b * a.S_max;

@@ -757,11 +757,8 @@ extern "C" int mla_append_fp8(const void* kv_new, const void* pe_new, const int3
   if (shift == 0)
     return launch_ex(append_fp8_rows_kernel, dim3((unsigned)ceil_div(N, kWarps)), dim3(kAppendThreads), 0, stream,
                      false, a);
-  // A CTA a token while all of them run at once (a decode step: every token
-  // leads its block); for more, eight tokens a CTA, of which few lead one.
-  const int per = N <= kWarps * info->sm_count ? 1 : kWarps;
-  return launch_ex(append_fp8_blocks_kernel, dim3((unsigned)ceil_div(N, per)), dim3(kAppendThreads), 0, stream, false,
-                   a, per);
+  return launch_ex(append_fp8_blocks_kernel, dim3((unsigned)append_blocks_grid(N, n_seq, shift)), dim3(kAppendThreads), 0,
+                   stream, false, a);
 }
 
 // ---------------------------------------------------------------- weights, eviction
@@ -832,9 +829,9 @@ int run_evict(const EvictBuffers& e, const int32_t* end_pos, int32_t* kept, int3
                    end_pos, S_max, keep, shift, ((S_max - 1) >> shift) + 1};
   if (in_place)
     return launch_cluster(evict_move_kernel<kFp8, true>, kMoveCluster, dim3(kMoveCluster, (unsigned)B),
-                          dim3(kMoveThreads), 0, stream, false, a);
+                          dim3(kMoveThreads), 0, stream, true, a);
   return launch_ex(evict_move_kernel<kFp8, false>, dim3((unsigned)ceil_div(keep, kMoveRows), (unsigned)B),
-                   dim3(kMoveThreads), 0, stream, false, a);
+                   dim3(kMoveThreads), 0, stream, true, a);
 }
 constexpr int kMaxEvictRows = 65535;  // grid y
 }  // namespace
