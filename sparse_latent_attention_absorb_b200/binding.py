@@ -133,8 +133,10 @@ def _ptr(t):
 
 
 def _stream(stream):
-    if stream is None:  # the raw handle: building a Stream object costs several microseconds
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    # the raw handle and device: a Stream object costs several microseconds,
+    # torch.cuda.current_device one (the calls' tensors have CUDA up by now)
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream
 
 
@@ -652,16 +654,17 @@ class Fp8Cache:
 
 
 def _check_same_device(device, **tensors):
-    if device.index != torch.cuda.current_device():
+    index = device.index
+    if index != torch._C._cuda_getDevice():
         raise ValueError(f"tensors on {device}, but the current device is cuda:{torch.cuda.current_device()}")
     for name, t in tensors.items():
-        if t is not None and t.device != device:
+        if t is not None and t.get_device() != index:
             raise ValueError(f"{name}: on {t.device}, expected {device}")
 
 
 def num_splits_fp8(R: int, K: int, n_heads: int = H) -> int:
     """mla_num_splits_fp8 for the current device (cached)."""
-    key = ("splits8", torch.cuda.current_device() if torch.cuda.is_available() else -1, R, K, n_heads)
+    key = ("splits8", torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1, R, K, n_heads)
     v = _sizing_cache.get(key)
     if v is None:
         v = _sizing_cache[key] = int(load_library().mla_num_splits_fp8(R, K, n_heads))
@@ -670,7 +673,7 @@ def num_splits_fp8(R: int, K: int, n_heads: int = H) -> int:
 
 def workspace_size_fp8(R: int, K: int, S_max: int, n_heads: int = H) -> int:
     """mla_sparse_decode_fp8_workspace_size for the current device (cached)."""
-    key = ("ws8", torch.cuda.current_device() if torch.cuda.is_available() else -1, R, K, S_max, n_heads)
+    key = ("ws8", torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1, R, K, S_max, n_heads)
     v = _sizing_cache.get(key)
     if v is None:
         v = _sizing_cache[key] = int(load_library().mla_sparse_decode_fp8_workspace_size(R, K, S_max, n_heads))
@@ -737,6 +740,8 @@ def mla_sparse_attend_fp8(q_lat, q_pe, cache: Fp8Cache, end_pos, topk_idx, scale
         lse_part = torch.empty((R, n_split, n_heads), dtype=torch.float32, device=q_lat.device)
     _check(o_part, "o_part", bf, (R, n_split, n_heads, D_LAT))
     _check(lse_part, "lse_part", torch.float32, (R, n_split, n_heads))
+    if d_status is not None:
+        _check(d_status, "d_status", torch.int32, (1,))
     _check_same_device(q_lat.device, q_pe=q_pe, cache=cache.kv, end_pos=end_pos, topk_idx=topk_idx,
                        cache_slot=cache_slot, o_part=o_part, lse_part=lse_part, d_status=d_status)
     rc = lib.mla_sparse_attend_fp8(_ptr(q_lat), _ptr(q_pe), _ptr(cache.kv), _ptr(cache.pe), _ptr(cache.scale),
