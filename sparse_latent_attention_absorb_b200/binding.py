@@ -834,8 +834,8 @@ def _evict_outputs(acc, end_pos, keep, recent, acc_out, kept, new_end, in_place,
             raise TypeError(f"{name}: expected an int")
     if not (1 <= keep <= S_max and 0 <= recent <= keep):
         raise ValueError(f"expected 1 <= keep <= {S_max} and 0 <= recent <= keep, got {keep} and {recent}")
-    if acc_out is None:
-        acc_out = acc if in_place else torch.empty_like(acc)
+    if in_place:
+        acc_out = acc
     _check(acc_out, "acc_out", torch.float32, (B, S_max))
     if kept is None:
         kept = torch.empty((B, keep), dtype=torch.int32, device=acc.device)
@@ -855,7 +855,7 @@ def mla_evict(kv_cache, pe_cache, acc, end_pos, keep: int, recent: int, kv_out=N
     Returns (kept int32 [B, keep], new_end int32 [B])."""
     lib = load_library()
     in_place = kv_out is None
-    if (pe_out is None) != in_place or (in_place and acc_out is not None):
+    if (pe_out is None) != in_place or (acc_out is None) != in_place:
         raise ValueError("kv_out, pe_out and acc_out: give all of them, or none (in place)")
     B, S_max, acc_out, kept, new_end = _evict_outputs(acc, end_pos, keep, recent, acc_out, kept, new_end, in_place,
                                                       kv_cache=kv_cache, pe_cache=pe_cache, kv_out=kv_out,
@@ -876,7 +876,7 @@ def mla_evict_fp8(cache: Fp8Cache, acc, end_pos, keep: int, recent: int, cache_o
     cache_out (of the same S_max and block) and acc_out."""
     lib = load_library()
     in_place = cache_out is None
-    if in_place and acc_out is not None:
+    if (acc_out is None) != in_place:
         raise ValueError("cache_out and acc_out: give both, or neither (in place)")
     to = cache if in_place else cache_out
     B, S_max, acc_out, kept, new_end = _evict_outputs(acc, end_pos, keep, recent, acc_out, kept, new_end, in_place,

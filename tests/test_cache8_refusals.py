@@ -116,6 +116,19 @@ def test_binding_refuses_cpu_tensors_and_bad_blocks():
         mla.mla_evict(kv, pe, torch.zeros(8), torch.zeros(1, dtype=torch.int32), 4, 1)
 
 
+def test_binding_eviction_takes_all_outputs_or_none():
+    """Out of place the totals move too: leaving their buffer out would drop them."""
+    kv, pe, acc = torch.zeros(1, 8, 512), torch.zeros(1, 8, 64), torch.zeros(1, 8)
+    end = torch.zeros(1, dtype=torch.int32)
+    for outs in (dict(kv_out=kv, pe_out=pe), dict(acc_out=acc), dict(kv_out=kv, acc_out=acc), dict(pe_out=pe)):
+        with pytest.raises(ValueError, match="all of them, or none"):
+            mla.mla_evict(kv, pe, acc, end, 4, 1, **outs)
+    cache = object.__new__(mla.Fp8Cache)
+    for outs in (dict(cache_out=cache), dict(acc_out=acc)):
+        with pytest.raises(ValueError, match="both, or neither"):
+            mla.mla_evict_fp8(cache, acc, end, 4, 1, **outs)
+
+
 def test_reference_rounding_is_torchs():
     """The tests' own E4M3 decoding and rounding against torch's cast: every code, its neighbours' midpoints, random numbers."""
     from tests import cache8_refs as ref
