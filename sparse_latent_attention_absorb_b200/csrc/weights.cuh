@@ -55,6 +55,7 @@ constexpr int kWtBlock = kWtNt * 128;
 __host__ __device__ constexpr int wt_blocks(bool fp8) { return fp8 ? 5 : 9; }  // a tile's: rotary, then latent
 __host__ __device__ constexpr int wt_group(bool fp8) { return fp8 ? 5 : 3; }   // blocks of a group
 __host__ __device__ constexpr int wt_groups(bool fp8) { return fp8 ? 2 : 4; }  // groups of the ring
+constexpr int kWtBox = 4;  // the query's eight boxes lie in the ring's blocks 4 .. 11 at first
 constexpr int kWtOffQpe = 12 * kWtBlock;
 constexpr int kWtOffScale = kWtOffQpe + kWtBlock;          // f32 [4][128]
 constexpr int kWtOffPos = kWtOffScale + 4 * kWtNt * 4;     // int [4][128], -1 = masked
@@ -154,18 +155,7 @@ accumulate_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __nv_b
       return f;
     };
     auto scale_of = [&](int p) -> float { return kFp8 && p >= 0 ? __ldg(sc_row + (p >> block_shift)) : 0.f; };
-    auto prefetch = [&](const Four& f) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (f.pos[i] < 0) continue;
-        const uint8_t* r = kv_row + (size_t)f.pos[i] * kRowBytes;
-#pragma unroll
-        for (int u = 0; u < kRowBytes / 128; ++u) asm volatile("prefetch.global.L2 [%0];" ::"l"(r + u * 128));
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(pe_row + (size_t)f.pos[i] * (kDr * 2)));
-      }
-    };
     Four cur = load(0), next = load(1);
-    prefetch(cur);
     float sv[4], sv_next[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) sv[i] = scale_of(cur.pos[i]);
@@ -181,7 +171,6 @@ accumulate_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __nv_b
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars->tile_full[j & 3]));
-      prefetch(next);
       cur = next;
       next = next2;
 #pragma unroll
@@ -196,7 +185,6 @@ accumulate_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __nv_b
     const uint32_t dst0 = s0 + sw128_offset(4 * g + (lane >> 3), lane & 7);
     int gr = 0;
     uint32_t ph = 1;
-    wait(smem_u32(&bars->q_full), 0, ab);  // the query's boxes lie in the ring until they are in TMEM
     for (int j = 0; j < n_tiles; ++j) {
       int pos[kCopies];
       const bool known = wait(smem_u32(&bars->tile_full[j & 3]), (j >> 2) & 1, ab);  // else timed out: nothing is read
@@ -205,6 +193,8 @@ accumulate_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __nv_b
 #pragma unroll 1
       for (int i = 0; i < kBlocks; ++i) {
         if (i % kGroup == 0) wait(smem_u32(&bars->empty[gr]), ph, ab);
+        // the query's boxes lie in the ring until they are in TMEM
+        if (j == 0 && gr * kGroup + i % kGroup == kWtBox) wait(smem_u32(&bars->q_full), 0, ab);
         const uint8_t* src = (i == 0 ? pe_row : kv_row + (i - 1) * 128) + (lane & 7) * 16;
         const uint32_t row_bytes = i == 0 ? kDr * 2 : kRowBytes;
         const uint32_t dst = dst0 + (gr * kGroup + i % kGroup) * kWtBlock;
@@ -222,7 +212,7 @@ accumulate_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __nv_b
       tma_prefetch_desc(&tm_q);
       mbar_arrive_expect_tx(smem_u32(&bars->q_tma), kH * kDl * 2);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) tma_load_3d(s0 + i * kWtBlock, &tm_q, smem_u32(&bars->q_tma), i * 64, 0, b);
+      for (int i = 0; i < 8; ++i) tma_load_3d(s0 + (kWtBox + i) * kWtBlock, &tm_q, smem_u32(&bars->q_tma), i * 64, 0, b);
 
       constexpr uint32_t id_16 = idesc_bf16_f32(128, kWtNt, false, false);
       constexpr uint32_t id_8 = idesc_e4m3_f32(128, kWtNt, false, false);
@@ -275,7 +265,7 @@ accumulate_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __nv_b
     const bool live = hd < n_heads;
     {
       // the query's row: 256 of its columns, and half of its rotary part
-      const uint32_t box = s0 + (uint32_t)(4 * ch) * kWtBlock + (uint32_t)hd * 128u;
+      const uint32_t box = s0 + (uint32_t)(kWtBox + 4 * ch) * kWtBlock + (uint32_t)hd * 128u;
       auto piece = [&](int c) {  // eight columns
         return ld_shared_v4(box + (uint32_t)(c >> 3) * kWtBlock + (uint32_t)(((c & 7) ^ (hd & 7)) << 4));
       };
@@ -308,20 +298,27 @@ accumulate_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __nv_b
         c2 *= exp2_int(-e);
         if (bad_s[hd] != 0.f) c2 = __int_as_float(0x7fffffff);
       }
-#pragma unroll 2
-      for (int c = 0; c < 32; c += 2) {
-        const uint4 a = piece(c), d = piece(c + 1);
-        const uint32_t w[8] = {a.x, a.y, a.z, a.w, d.x, d.y, d.z, d.w};
-        if (kFp8) {
-          uint32_t hi[4], lo[4];
+      // the loads first, so that their latency is met once a round
+      constexpr int kRound = kFp8 ? 8 : 4;  // pieces
+#pragma unroll 1
+      for (int c = 0; c < 32; c += kRound) {
+        uint4 v[kRound];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) limbs4(w[2 * u], w[2 * u + 1], mul * (1.f / 256.f), 1.f, &hi[u], &lo[u]);
-          tmem_st4(tmem + lane_base + kWtColQ + 64 * ch + 2 * c, hi);
-          tmem_st4(tmem + lane_base + kWtColQ + 128 + 64 * ch + 2 * c, lo);
+        for (int q = 0; q < kRound; ++q) v[q] = piece(c + q);
+        uint32_t r[16];
+        if constexpr (kFp8) {
+          uint32_t lo[16];
+#pragma unroll
+          for (int q = 0; q < kRound; ++q) {
+            limbs4(v[q].x, v[q].y, mul * (1.f / 256.f), 1.f, &r[2 * q], &lo[2 * q]);
+            limbs4(v[q].z, v[q].w, mul * (1.f / 256.f), 1.f, &r[2 * q + 1], &lo[2 * q + 1]);
+          }
+          tmem_st16(tmem + lane_base + kWtColQ + 64 * ch + 2 * c, r);
+          tmem_st16(tmem + lane_base + kWtColQ + 128 + 64 * ch + 2 * c, lo);
         } else {
-          const uint32_t x[4] = {w[0], w[1], w[2], w[3]}, z[4] = {w[4], w[5], w[6], w[7]};
-          tmem_st4(tmem + lane_base + kWtColQ + 128 * ch + 4 * c, x);
-          tmem_st4(tmem + lane_base + kWtColQ + 128 * ch + 4 * c + 4, z);
+#pragma unroll
+          for (int q = 0; q < kRound; ++q) r[4 * q] = v[q].x, r[4 * q + 1] = v[q].y, r[4 * q + 2] = v[q].z, r[4 * q + 3] = v[q].w;
+          tmem_st16(tmem + lane_base + kWtColQ + 128 * ch + 4 * c, r);
         }
       }
       tmem_wait_st();
