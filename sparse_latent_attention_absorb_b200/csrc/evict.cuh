@@ -9,8 +9,11 @@
 //                        the kept positions; the totals move along
 //   evict_move_kernel    the rows
 //
-// Bound: the select reads a row's totals five times from L1 and L2, the move is
-// HBM traffic.
+// Bound: the selection by its chain of passes (a row is one CTA, of a few long
+// rows a cluster of eight: 64 rows of 8192 take about 13 us, 27000 cycles of
+// which 6300 are the first read of the totals and their histogram, 4600 the
+// numbering), the move by HBM (64 rows of 8192 keeping 4096 in 8 bits, 209 MB:
+// 38 us, 5.5 TB/s).  The move's CTAs come up while the selection runs.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -22,7 +25,7 @@ namespace mla {
 
 constexpr int kSelectThreads = 1024;
 constexpr int kSelectBins = 2048;
-constexpr int kSelectUnroll = 4;  // independent loads of a thread
+constexpr int kSelectHold = 8;  // totals that a thread holds
 constexpr int kSelectCluster = 8;
 
 // Bits whose unsigned order is the weights' order, NaN above all, the two zeros
@@ -90,7 +93,25 @@ evict_select_kernel(const float* acc, const int32_t* __restrict__ end_pos, float
   } else {
     const int seg = (n + n_cta * 1024 - 1) / (n_cta * 1024) * 1024;  // a CTA's positions
     const int s0 = min(n, rank * seg), s1 = min(n, s0 + seg);
-    const int l1 = min(s1, late);
+    // A warp takes 1/32 of the CTA's positions, 32 at a time.  Up to 8192
+    // positions of a CTA stay in registers through all passes; of more, each
+    // pass reads them again (from L1 and L2).
+    const int run = seg / 32;
+    const int i0 = min(s1, s0 + (tid >> 5) * run), i1 = min(s1, i0 + run);
+    float x[kSelectHold];
+    bool held = false;
+    auto fetch = [&](int i) {
+      if (held) return;
+#pragma unroll
+      for (int u = 0; u < kSelectHold; ++u) x[u] = i + 32 * u + lane < i1 ? w[i + 32 * u + lane] : 0.f;
+      held = run <= 32 * kSelectHold;
+    };
+    auto sync_row = [&]() {
+      if (n_cta > 1)
+        cluster_sync();
+      else
+        __syncthreads();
+    };
     // the key of rank `left` (from 1, largest first) among [0, late)
     uint32_t prefix = 0, mask = 0;
     int left = keep - min(recent, keep);  // how many of [0, late) stay
@@ -100,17 +121,13 @@ evict_select_kernel(const float* acc, const int32_t* __restrict__ end_pos, float
         const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), width = pass == 2 ? 10 : 11;
         for (int i = tid; i < kSelectBins; i += kSelectThreads) bins[i] = 0;
         __syncthreads();
-        for (int i0 = s0; i0 < l1; i0 += kSelectUnroll * kSelectThreads) {
-          float x[kSelectUnroll];
+        for (int i = i0; i < i1; i += 32 * kSelectHold) {
+          fetch(i);
 #pragma unroll
-          for (int u = 0; u < kSelectUnroll; ++u) {
-            const int i = i0 + u * kSelectThreads + tid;
-            x[u] = i < l1 ? w[i] : 0.f;
-          }
-#pragma unroll
-          for (int u = 0; u < kSelectUnroll; ++u) {
+          for (int u = 0; u < kSelectHold; ++u) {
+            if (i + 32 * u >= i1) break;
             const uint32_t k = weight_key(x[u]);
-            const bool in = i0 + u * kSelectThreads + tid < l1 && (k & mask) == prefix;
+            const bool in = i + 32 * u + lane < min(i1, late) && (k & mask) == prefix;
             const uint32_t bin = (k >> shift) & ((1u << width) - 1u);
             // equal weights (never selected: 0) would queue up at one bin: the
             // lanes that share the first lane's bin count as one
@@ -125,7 +142,7 @@ evict_select_kernel(const float* acc, const int32_t* __restrict__ end_pos, float
             }
           }
         }
-        cluster_sync();
+        sync_row();
         // bins from the top, of all CTAs: thread t holds bins 2047 - 2t and 2046 - 2t
         const int b0 = kSelectBins - 1 - 2 * tid;
         const uint32_t* sums = bins;
@@ -156,27 +173,21 @@ evict_select_kernel(const float* acc, const int32_t* __restrict__ end_pos, float
     } else {
       prefix = 0xffffffffu;  // no key is larger, and none of the ties stays
     }
-    // Above the key, or one of its first `left` ties, or late.  A warp takes
-    // 1/32 of the CTA's positions, 32 at a time, and counts them; the sums over
-    // the warps and CTAs before it tell it where its own go.
-    const int run = seg / 32;
-    const int i0 = min(s1, s0 + (tid >> 5) * run), i1 = min(s1, i0 + run);
+    // Above the key, or one of its first `left` ties, or late: every warp counts
+    // its own, and the sums over the warps and CTAs before it tell it where they
+    // go.
     // the lanes of a step whose position is above the key, and its ties
-    auto look = [&](float x, int i, uint32_t* above, uint32_t* ties) {
-      const uint32_t k = weight_key(x);
+    auto look = [&](float v, int i, uint32_t* above, uint32_t* ties) {
+      const uint32_t k = weight_key(v);
       *above = __ballot_sync(0xffffffffu, i < i1 && (i >= late || k > prefix));
       *ties = __ballot_sync(0xffffffffu, i < i1 && i < late && k == prefix);
     };
-    auto load = [&](float (&x)[kSelectUnroll], int i) {
-#pragma unroll
-      for (int u = 0; u < kSelectUnroll; ++u) x[u] = i + 32 * u + lane < i1 ? w[i + 32 * u + lane] : 0.f;
-    };
     int2 c = make_int2(0, 0);
-    for (int i = i0; i < i1; i += 32 * kSelectUnroll) {
-      float x[kSelectUnroll];
-      load(x, i);
+    for (int i = i0; i < i1; i += 32 * kSelectHold) {
+      fetch(i);
 #pragma unroll
-      for (int u = 0; u < kSelectUnroll; ++u) {
+      for (int u = 0; u < kSelectHold; ++u) {
+        if (i + 32 * u >= i1) break;
         uint32_t above, ties;
         look(x[u], i + 32 * u + lane, &above, &ties);
         c.x += __popc(above), c.y += __popc(ties);
@@ -186,17 +197,17 @@ evict_select_kernel(const float* acc, const int32_t* __restrict__ end_pos, float
     int2 at = block_scan2(lane == 31 ? c : make_int2(0, 0), warp_sums, &total);
     at.x = __shfl_sync(0xffffffffu, at.x, 0), at.y = __shfl_sync(0xffffffffu, at.y, 0);
     if (tid == 0) counts = total;
-    cluster_sync();
+    sync_row();
     for (int r = 0; r < rank; ++r) {
       const uint32_t far = cluster_map(smem_u32(&counts), (uint32_t)r);
       at.x += (int)ld_cluster_u32(far), at.y += (int)ld_cluster_u32(far + 4);
     }
     const uint32_t below = (1u << lane) - 1u;
-    for (int i = i0; i < i1; i += 32 * kSelectUnroll) {
-      float x[kSelectUnroll];
-      load(x, i);
+    for (int i = i0; i < i1; i += 32 * kSelectHold) {
+      fetch(i);
 #pragma unroll
-      for (int u = 0; u < kSelectUnroll; ++u) {
+      for (int u = 0; u < kSelectHold; ++u) {
+        if (i + 32 * u >= i1) break;
         uint32_t above, ties;
         look(x[u], i + 32 * u + lane, &above, &ties);
         const int tie = at.y + __popc(ties & below);
@@ -214,7 +225,10 @@ evict_select_kernel(const float* acc, const int32_t* __restrict__ end_pos, float
   if (apart) {
     for (int i = n_new + me; i < S_max; i += all) out[i] = 0.f;
   }
-  cluster_sync();  // kept is whole, and no CTA reads another's memory any more
+  if (n_cta > 1)
+    cluster_sync();  // kept is whole, and no CTA reads another's memory any more
+  else
+    __syncthreads();
   if (apart || rank != 0) return;
   // In place, one CTA: what a step writes, [i0, i0 + 1024), no later step
   // reads, and its own reads are done.
