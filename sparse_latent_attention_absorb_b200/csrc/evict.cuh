@@ -12,7 +12,7 @@
 // Bound: the selection by its chain of passes (a row is one CTA, of a few long
 // rows a cluster of eight: 64 rows of 8192 take about 13 us, 27000 cycles of
 // which 6300 are the first read of the totals and their histogram, 4600 the
-// numbering), the move by HBM (64 rows of 8192 keeping 4096 in 8 bits, 209 MB:
+// numbering), the move by HBM (64 rows of up to 8192 keeping 2500 in 8 bits, 209 MB:
 // 38 us, 5.5 TB/s).  The move's CTAs come up while the selection runs.
 #pragma once
 

@@ -141,6 +141,27 @@ def test_append_slots_many_sequences_and_streams():
     assert torch.equal(c.kv, want[0]) and torch.equal(c.scale, want[2]) and torch.equal(c.pe, want[1])
 
 
+@pytest.mark.parametrize("block", [2, 16, 128])
+def test_append_many_ragged_sequences(block):
+    """Runs of 0 to 40 tokens that start anywhere, over both ends too: a block is written by one run, whole or in part."""
+    g = gen(17 + block)
+    n = 150
+    c = make_cache(g, n, 60, block)
+    new = torch.randint(0, 41, (n,), generator=g, device=DEV).tolist()
+    start = torch.randint(-10, 65, (n,), generator=g, device=DEV).tolist()
+    cu = [0]
+    for k in new:
+        cu.append(cu[-1] + k)
+    N = cu[-1] + 40
+    x = (torch.randn(N, 512, generator=g, device=DEV) * torch.exp2(torch.randint(-6, 7, (N, 1), generator=g, device=DEV).float())).to(bf)
+    r = torch.randn(N, 64, generator=g, device=DEV).to(bf)
+    want = [t.clone() for t in (c.kv, c.pe, c.scale)]
+    ref.append(*want, block, x, r, cu, start)
+    mla.mla_append_fp8(c, x, r, torch.tensor(cu, dtype=torch.int32, device=DEV), torch.tensor(start, dtype=torch.int32, device=DEV))
+    assert torch.equal(c.kv, want[0]) and torch.equal(c.scale, want[2])
+    assert torch.equal(c.pe.view(torch.int16), want[1].view(torch.int16))
+
+
 # ------------------------------------------------------------------- attention
 def score_bound(q_lat, q_pe, cache, slot, t, limb):
     """How far a score may be from the 64-bit one, [h, t]."""
@@ -345,6 +366,47 @@ def test_decode_graph_streams_and_repeats():
         torch.cuda.current_stream().wait_stream(side)
         assert torch.equal(out, first)
     torch.testing.assert_close(other.float(), first[:3].float(), rtol=2.0 ** -6, atol=1e-3)  # another split of the keys
+
+
+def test_steps_at_once():
+    """Calls on two streams that overlap on the GPU (pairs and single CTAs, totals, appends) answer as they do alone."""
+    g = gen(77)
+    c = make_cache(g, 4, 500, 8)
+    end = torch.tensor([500, 300, 129, 7], dtype=torch.int32, device=DEV)
+    idx = selection(g, end.tolist(), 400, 500)
+    args = []
+    for h in (128, 40):
+        q, w = torch.randn(4, h, 128, generator=g, device=DEV).to(bf), (torch.randn(h * 256, 512, generator=g, device=DEV) * 512 ** -0.5).to(bf)
+        args.append((q, torch.randn(4, h, 64, generator=g, device=DEV).to(bf), w, torch.empty(4, h, device=DEV)))
+    x, r = torch.randn(4, 512, generator=g, device=DEV).to(bf), torch.randn(4, 64, generator=g, device=DEV).to(bf)
+    cu, at = torch.arange(5, dtype=torch.int32, device=DEV), torch.tensor([499, 300, 130, 9], dtype=torch.int32, device=DEV)
+
+    def step(i, cache):
+        q, pe, w, lse = args[i]
+        status = torch.zeros(1, dtype=torch.int32, device=DEV)
+        out = mla.mla_sparse_decode_fp8(q, pe, c, end, idx, w, SCALE, lse_out=lse, d_status=status)
+        acc = torch.zeros(4, 500, device=DEV)
+        mla.mla_accumulate_weights_fp8((q.float() @ torch.ones(128, 512, device=DEV) / 128).to(bf), pe, c, end, idx, SCALE, lse, acc)
+        mla.mla_append_fp8(cache, x, r, cu, at)
+        return out, lse.clone(), acc, cache.kv.clone(), cache.scale.clone(), status
+
+    def copy():
+        return mla.Fp8Cache(c.kv.clone(), c.pe.clone(), c.scale.clone(), c.block)
+
+    alone = [step(i, copy()) for i in range(2)]
+    sides, copies = [torch.cuda.Stream(), torch.cuda.Stream()], [[copy() for _ in range(6)] for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for k in range(6):
+        for i in range(2):
+            with torch.cuda.stream(sides[i]):
+                got[i].append(step(i, copies[i][k]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for one in got[i]:
+            assert int(one[-1]) == 0
+            for a, b in zip(one, alone[i]):
+                assert torch.equal(a, b)
 
 
 def test_decode_index_checks():
