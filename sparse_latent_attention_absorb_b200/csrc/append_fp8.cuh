@@ -151,15 +151,16 @@ append_fp8_rows_kernel(const AppendArgs a) {
 
 // Shared scales: a CTA per block of positions, all warps at its rows, up to
 // kHold rows of a warp held in registers between the maximum and the rounding
-// (the others are read twice, the second time from L1 or L2).
+// (the others are read twice, the second time from L1 or L2): two where a block
+// has no more (16 positions), and six CTAs an SM then, else four.
 //
 // Sequence q's blocks are the CTAs from cu[q] / block + 2 q on: L tokens touch
 // at most L / block + 2 blocks, so they end before the next sequence's, and the
 // CTAs behind them return.
-constexpr int kHold = 4;
 __host__ __device__ inline int append_blocks_grid(int N, int n_seq, int shift) { return (N >> shift) + 2 * n_seq; }
 
-__global__ void __launch_bounds__(kAppendThreads)
+template <int kHold>
+__global__ void __launch_bounds__(kAppendThreads, kHold == 2 ? 6 : 4)
 append_fp8_blocks_kernel(const AppendArgs a) {
   constexpr int kWarps = kAppendThreads / 32;
   __shared__ float tops[kWarps];

@@ -757,8 +757,8 @@ extern "C" int mla_append_fp8(const void* kv_new, const void* pe_new, const int3
   if (shift == 0)
     return launch_ex(append_fp8_rows_kernel, dim3((unsigned)ceil_div(N, kWarps)), dim3(kAppendThreads), 0, stream,
                      false, a);
-  return launch_ex(append_fp8_blocks_kernel, dim3((unsigned)append_blocks_grid(N, n_seq, shift)), dim3(kAppendThreads), 0,
-                   stream, false, a);
+  return launch_ex(shift <= 4 ? append_fp8_blocks_kernel<2> : append_fp8_blocks_kernel<4>,
+                   dim3((unsigned)append_blocks_grid(N, n_seq, shift)), dim3(kAppendThreads), 0, stream, false, a);
 }
 
 // ---------------------------------------------------------------- weights, eviction
