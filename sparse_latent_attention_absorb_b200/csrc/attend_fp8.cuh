@@ -54,26 +54,38 @@ __device__ __forceinline__ int limb_exponent(float amax) {
   int k;
   const float m = frexpf(amax, &k);          // amax = m 2^k, m in [1/2, 1)
   const int e = (m <= 0.875f ? 9 : 8) - k;   // 448 = 0.875 2^9
-  return e < -100 ? -100 : (e > 100 ? 100 : e);
+  return e < -118 ? -118 : (e > 118 ? 118 : e);  // 2^(e - 8) and 2^-e are normal
 }
 __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }  // |e| <= 126
 
-// Four bf16 query factors x as limbs: x 2^e = hi + lo / lo_scale, `mul` =
-// 2^(e - 8).  A second limb that is scaled up by 16 keeps its bits however small
+// Four query factors x as limbs, from fp16 numbers 2^(e - 8) x: x 2^e = hi + lo /
+// lo_scale.  A second limb that is scaled up by 16 keeps its bits however small
 // x is: a bf16 x is met exactly (4 + 4 signed bits) down to 2^-17 of the
 // largest; one that is not, down to 2^-10, and to 2^-19 of the largest below.
 constexpr float kLimbLo = 1.f / 16.f;
-__device__ __forceinline__ void limbs4(uint32_t x01, uint32_t x23, float mul, float lo_scale, uint32_t* hi, uint32_t* lo) {
+__device__ __forceinline__ void limbs4_half(uint32_t f01, uint32_t f23, float lo_scale, uint32_t* hi, uint32_t* lo) {
   uint32_t first[2], rest[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const uint32_t x = i ? x23 : x01;
-    const uint32_t f = half2_bits(__floats2half2_rn(__uint_as_float(x << 16) * mul, __uint_as_float(x & 0xffff0000u) * mul));
+    const uint32_t f = i ? f23 : f01;
     first[i] = limb_first(f);
     rest[i] = limb_first(half2_bits(__hmul2(limb_rest(f, first[i]), __float2half2_rn(lo_scale))));
   }
   *hi = limb_bytes(first[0], first[1]);
   *lo = limb_bytes(rest[0], rest[1]);
+}
+// The same from bf16 numbers x, `mul` = 2^(e - 8).
+__device__ __forceinline__ uint32_t half2_of_bf16(uint32_t x, float mul) {
+  return half2_bits(__floats2half2_rn(__uint_as_float(x << 16) * mul, __uint_as_float(x & 0xffff0000u) * mul));
+}
+__device__ __forceinline__ void limbs4(uint32_t x01, uint32_t x23, float mul, float lo_scale, uint32_t* hi, uint32_t* lo) {
+  limbs4_half(half2_of_bf16(x01, mul), half2_of_bf16(x23, mul), lo_scale, hi, lo);
+}
+// 2^x as two fp16 numbers (0 below 2^-24, 2^15 above it).
+__device__ __forceinline__ __half2 half2_power(int x) {
+  const uint32_t b = x >= -14 ? (uint32_t)(min(x, 15) + 15) << 10 : (x >= -24 ? 1u << (x + 24) : 0u);
+  const uint32_t w = b | (b << 16);
+  return *reinterpret_cast<const __half2*>(&w);
 }
 
 // The magnitudes' bits of two bf16 numbers, each the larger of m's and x's.
@@ -206,7 +218,8 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t at) {
 
 template <bool kPair>
 __global__ void __launch_bounds__(kF8Threads, 1)
-sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __nv_bfloat16* __restrict__ q_pe,
+sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const uint8_t* q_exp, int n_rows,
+                         const __nv_bfloat16* __restrict__ q_pe,
                          const uint8_t* __restrict__ kv8, const __nv_bfloat16* __restrict__ pe8,
                          const float* __restrict__ kv_scale, int block_shift, int n_blocks,
                          const int32_t* __restrict__ end_pos, const int32_t* __restrict__ topk_idx, float scale,
@@ -562,20 +575,38 @@ sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __nv_bf
 #pragma unroll
       for (int u = 0; u < 4; ++u) r4[u] = hi_row && hd < live ? __ldg(psrc + u) : make_uint4(0, 0, 0, 0);
 
+      // scaled (fp16): the exponents of the thread's two times 128 columns
+      const bool scaled = q_exp != nullptr;
+      int ex[2] = {0, 0};
+      if (scaled) {
+        grid_dep_wait();
+        if (hd < live) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) ex[i] = 127 - (int)__ldcg(q_exp + (size_t)((h0 + hd) * 4 + 2 * ch + i) * n_rows + b);
+        }
+      }
+
       wait(smem_u32(&bars->q_tma), 0, ab);
-      uint32_t m2 = 0;
-#pragma unroll 8
-      for (int c = 0; c < 16; ++c) {  // the two rows of a head share its columns
-        const uint4 v = piece(2 * c + (hi_row ? 0 : 1));
-        m2 = amax2(amax2(amax2(amax2(m2, v.x), v.y), v.z), v.w);
+      float top = 0.f;
+      bool finite = true;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint32_t m2 = 0;
+#pragma unroll
+        for (int c = 8 * i; c < 8 * i + 8; ++c) {  // the two rows of a head share its columns
+          const uint4 v = piece(2 * c + (hi_row ? 0 : 1));
+          m2 = amax2(amax2(amax2(amax2(m2, v.x), v.y), v.z), v.w);
+        }
+        const uint32_t m = max(m2 & 0xffffu, m2 >> 16);
+        finite &= m < (scaled ? 0x7c00u : 0x7f80u);
+        top = fmaxf(top, scaled ? __half2float(__ushort_as_half((unsigned short)m)) * exp2_int(ex[i]) : __uint_as_float(m << 16));
       }
-      uint32_t m = max(m2 & 0xffffu, m2 >> 16);
-      if (m >= 0x7f80u) {  // an infinity or NaN: the head's scores are NaN, the others' scale is not its
+      if (!finite) {  // an infinity or NaN: the head's scores are NaN, the others' scale is not its
         fin[hd] = 1.f;
-        m = 0;
+        top = 0.f;
       }
-      m = __reduce_max_sync(0xffffffffu, m);
-      if (lane == 0) red[warp] = __uint_as_float(m << 16);
+      top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+      if (lane == 0) red[warp] = top;
       named_bar_sync(1, kSoftmaxThreads);
       bad = fin[hd] != 0.f;
       float am = red[0];
@@ -601,13 +632,28 @@ sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const __nv_bf
         uint4 v[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) v[q] = piece(8 * c4 + 2 * q + (hi_row ? 0 : 1));
+        // as fp16 numbers 2^(e - 8) x
+        if (scaled) {
+          const __half2 to = half2_power((c4 < 2 ? ex[0] : ex[1]) + e - 8);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            auto times = [&](uint32_t h) { return half2_bits(__hmul2(*reinterpret_cast<const __half2*>(&h), to)); };
+            v[q] = make_uint4(times(v[q].x), times(v[q].y), times(v[q].z), times(v[q].w));
+          }
+        } else {
+          const float to = mul * (1.f / 256.f);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            v[q] = make_uint4(half2_of_bf16(v[q].x, to), half2_of_bf16(v[q].y, to), half2_of_bf16(v[q].z, to),
+                              half2_of_bf16(v[q].w, to));
+        }
         uint32_t keep[8], send[8], r[16];
 #pragma unroll
         for (int q = 0; q < 4; ++q)
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             uint32_t hi, lo;
-            limbs4(u ? v[q].z : v[q].x, u ? v[q].w : v[q].y, mul * (1.f / 256.f), 1.f / kLimbLo, &hi, &lo);
+            limbs4_half(u ? v[q].z : v[q].x, u ? v[q].w : v[q].y, 1.f / kLimbLo, &hi, &lo);
             keep[2 * q + u] = hi_row ? hi : lo;
             send[2 * q + u] = hi_row ? lo : hi;
           }

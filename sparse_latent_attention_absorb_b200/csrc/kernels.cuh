@@ -81,9 +81,18 @@ __device__ unsigned long long g_mla_kernel_ns[kKernelEvents];
   } while (0)
 #endif
 
+// kScaled: q_lat as fp16 in units of a power of two for each row and 128
+// columns, for the 8-bit attention, which splits it into limbs of nine bits
+// together (rounded to bf16's eight it would be the largest error of that decode
+// step).  The power comes from a bound that costs no look at the results, |q_lat|
+// <= 128 max|q_nope[b,h]| max|W_UK[h, :, chunk]| (of the row itself and of the
+// weights: rows stay independent), which fp16 sees below 2^4; a result 2^12 below
+// its bound still keeps bf16's digits.  q_exp [n_heads, 4, B]: result = fp16
+// 2^(127 - q_exp).
+template <bool kScaled>
 __global__ void __launch_bounds__(128, 1)
 absorb_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_q,
-              __nv_bfloat16* __restrict__ q_lat, int B, int n_tile, int n_heads, int* d_status) {
+              void* __restrict__ q_lat, uint8_t* __restrict__ q_exp, int B, int n_tile, int n_heads, int* d_status) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = align_smem_1024(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -144,6 +153,39 @@ absorb_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ 
   }
   __syncwarp();
 
+  __shared__ __align__(16) float row_scale[kScaled ? kAbsorbNMax : 1];
+  __shared__ uint32_t top_w[4];
+  if constexpr (kScaled) {
+    wait(bar_load, 0, ab);
+    // thread t: row t of the 128 of W_UK, and row t of the queries, two blocks of
+    // 128 bytes each (in an order of its own: no two lanes at a bank)
+    auto top = [&](uint32_t at, uint32_t next) {
+      uint32_t m[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        uint32_t x[4];
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                     : "r"(at + (i >> 3) * next + (((uint32_t)i ^ (uint32_t)tid) & 7u) * 16u));
+#pragma unroll
+        for (int u = 0; u < 4; ++u) m[u] = __vmaxu2(m[u], x[u] & 0x7fff7fffu);
+      }
+      const uint32_t all = __vmaxu2(__vmaxu2(m[0], m[1]), __vmaxu2(m[2], m[3]));
+      return max(all & 0xffffu, all >> 16) >> 7;  // the biased exponent
+    };
+    const uint32_t w = __reduce_max_sync(0xffffffffu, top(sA + tid * 128, 64 * 128 * 2));
+    if (lane == 0) top_w[warp] = w;
+    const uint32_t q = tid < n_tile ? top(sB + tid * 128, n_tile * 128) : 0u;
+    __syncthreads();
+    const int e_w = (int)max(max(top_w[0], top_w[1]), max(top_w[2], top_w[3]));
+    const int up = min(max(249 - (int)q - e_w, -126), 126);
+    if (tid < n_tile) {
+      row_scale[tid] = __uint_as_float((uint32_t)(127 + up) << 23);
+      if (b0 + tid < B) q_exp[(size_t)(h * (kDl / 128) + chunk) * B + b0 + tid] = (uint8_t)(127 + up);
+    }
+    __syncthreads();
+  }
+
   // Epilogue: lane (32*warp + lane) holds column c of the chunk, one TMEM
   // column per batch row.
   wait(bar_mma, 0, ab);
@@ -153,10 +195,20 @@ absorb_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ 
     uint32_t v[16];
     tmem_ld16(tmem + ((uint32_t)(warp * 32) << 16) + n0, v);
     tmem_wait_ld();
+    float up[16];  // (read before the stores, which might alias them for all the compiler knows: 13 us of 44 at 500 rows)
+    if constexpr (kScaled) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) up[j] = row_scale[n0 + j];
+    }
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
       const int b = b0 + n0 + j;
-      if (b < B) q_lat[((size_t)b * n_heads + h) * kDl + c] = __float2bfloat16_rn(__uint_as_float(v[j]));
+      const size_t at = ((size_t)b * n_heads + h) * kDl + c;
+      if constexpr (kScaled) {
+        if (b < B) static_cast<__half*>(q_lat)[at] = __float2half_rn(__uint_as_float(v[j]) * up[j]);
+      } else {
+        if (b < B) static_cast<__nv_bfloat16*>(q_lat)[at] = __float2bfloat16_rn(__uint_as_float(v[j]));
+      }
     }
   }
   tc_fence_before();

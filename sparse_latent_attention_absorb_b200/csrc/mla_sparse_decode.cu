@@ -46,7 +46,8 @@ DeviceInfo g_dev[kMaxDevices];
 
 cudaError_t configure_cache_kernels() {
   constexpr auto kAttr = cudaFuncAttributeMaxDynamicSharedMemorySize;
-  cudaError_t e = cudaFuncSetAttribute(sparse_attend_fp8_kernel<true>, kAttr, kF8SmemBytes);
+  cudaError_t e = cudaFuncSetAttribute(absorb_kernel<true>, kAttr, kAbsorbSmemBytes);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(sparse_attend_fp8_kernel<true>, kAttr, kF8SmemBytes);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(sparse_attend_fp8_kernel<false>, kAttr, kF8SmemBytes);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(accumulate_weights_kernel<false>, kAttr, kWtSmemBytes);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(accumulate_weights_kernel<true>, kAttr, kWtSmemBytes);
@@ -67,7 +68,7 @@ int current_device(DeviceInfo** info) {
     d.sm100 = (major == 10 && minor == 0);
     d.sm_count = sms;
     if (d.sm100) {
-      if (cudaFuncSetAttribute(absorb_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAbsorbSmemBytes) != cudaSuccess ||
+      if (cudaFuncSetAttribute(absorb_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kAbsorbSmemBytes) != cudaSuccess ||
           cudaFuncSetAttribute(sparse_attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttendSmemBytes) != cudaSuccess ||
           configure_cache_kernels() != cudaSuccess ||
           cudaFuncSetAttribute(combine_value_up_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCombineSmemBytes) != cudaSuccess ||
@@ -348,16 +349,17 @@ int launch_ex(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cuda
   return launch_cluster(kernel, 0, grid, block, smem, stream, pdl, args...);
 }
 
+// With q_exp, q_lat in the 8-bit attention's scaled form (absorb_kernel<true>).
 int launch_absorb(const void* q_nope, const void* wkv_b, void* q_lat, int B, int* d_status, cudaStream_t stream,
-                  int n_heads = kH) {
+                  int n_heads = kH, uint8_t* q_exp = nullptr) {
   const int n_tile = B >= kAbsorbNMax ? kAbsorbNMax : ceil_div(B, 16) * 16;
   CUtensorMap tm_w, tm_q;
   int rc;
   if ((rc = encode_wkv_b(&tm_w, wkv_b, n_heads)) != MLA_OK) return rc;
   if ((rc = encode_q_nope(&tm_q, q_nope, B, n_tile, n_heads)) != MLA_OK) return rc;
   dim3 grid(kDl / 128, n_heads, ceil_div(B, kAbsorbNMax));
-  return launch_ex(absorb_kernel, grid, dim3(128), absorb_smem_bytes(n_tile), stream, false, tm_w, tm_q,
-                   static_cast<__nv_bfloat16*>(q_lat), B, n_tile, n_heads, d_status);
+  return launch_ex(q_exp ? absorb_kernel<true> : absorb_kernel<false>, grid, dim3(128), absorb_smem_bytes(n_tile), stream,
+                   false, tm_w, tm_q, q_lat, q_exp, B, n_tile, n_heads, d_status);
 }
 
 int launch_attend(const void* q_lat, const void* q_pe, const void* kv_cache, const void* pe_cache,
@@ -380,7 +382,8 @@ int launch_attend(const void* q_lat, const void* q_pe, const void* kv_cache, con
 int launch_attend_fp8(const void* q_lat, const void* q_pe, const void* kv_fp8, const void* pe, const float* kv_scale,
                       int shift, const int32_t* cache_slot, const int32_t* end_pos, const int32_t* topk_idx,
                       float scale, void* o_part, float* lse_part, int R, int K, int S_max, int n_slots, int n_heads,
-                      int n_split, int span, const void* w_next, int* d_status, cudaStream_t stream, bool pdl) {
+                      int n_split, int span, const void* w_next, int* d_status, cudaStream_t stream, bool pdl,
+                      const uint8_t* q_exp = nullptr) {
   const int per = fp8_ctas(n_heads);
   const long long ctas = (long long)R * n_split * per;
   if (ctas > 0x7fffffffLL) return MLA_ERR_INVALID_ARG;
@@ -390,7 +393,7 @@ int launch_attend_fp8(const void* q_lat, const void* q_pe, const void* kv_fp8, c
   if ((rc = encode_q_half(&tm_q, q_lat, R, n_heads, kDl, 64, CU_TENSOR_MAP_SWIZZLE_128B, kF8Heads)) != MLA_OK) return rc;
   auto go = [&](auto kernel) {
     return launch_cluster(kernel, (unsigned)per, dim3((unsigned)ctas), dim3(kF8Threads), kF8SmemBytes, stream, pdl,
-                          tm_q, static_cast<const __nv_bfloat16*>(q_pe),
+                          tm_q, q_exp, R, static_cast<const __nv_bfloat16*>(q_pe),
                           static_cast<const uint8_t*>(kv_fp8), static_cast<const __nv_bfloat16*>(pe), kv_scale, shift,
                           n_blocks, end_pos, topk_idx, scale, static_cast<__nv_bfloat16*>(o_part), lse_part, K, S_max,
                           n_split, span, static_cast<const __nv_bfloat16*>(w_next), cache_slot, n_slots, n_heads,
@@ -668,11 +671,14 @@ extern "C" int mla_num_splits_fp8(int R, int K, int n_heads) {
   return n_split;
 }
 
+// The scaled queries' exponents lie behind the rest of the workspace.
+static size_t q_exp_bytes(int R, int n_heads) { return round_up((size_t)R * n_heads * (kDl / 128), 256); }
+
 extern "C" size_t mla_sparse_decode_fp8_workspace_size(int R, int K, int S_max, int n_heads) {
   if (!sizes_ok(R, K, S_max) || n_heads < 1 || n_heads > kH) return 0;
   int n_split = 0, span = 0;
   plan_splits_fp8(R, K, n_heads, planning_sm_count(), &n_split, &span);
-  return workspace_layout(R, n_split, n_heads).total;
+  return workspace_layout(R, n_split, n_heads).total + q_exp_bytes(R, n_heads);
 }
 
 extern "C" int mla_sparse_attend_fp8(const void* q_lat, const void* q_pe, const void* kv_fp8, const void* pe,
@@ -719,19 +725,21 @@ extern "C" int mla_sparse_decode_fp8(const void* q_nope, const void* q_pe, const
   int n_split = 0, span = 0;
   plan_splits_fp8(R, K, n_heads, info->sm_count, &n_split, &span);
   const WorkspaceLayout wl = workspace_layout(R, n_split, n_heads);
-  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < wl.total)
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
+      workspace_bytes < wl.total + q_exp_bytes(R, n_heads))
     return MLA_ERR_WORKSPACE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   void* q_lat = ws + wl.q_lat;
   void* o_part = ws + wl.o_part;
   float* lse_part = reinterpret_cast<float*>(ws + wl.lse_part);
+  uint8_t* q_exp = ws + wl.total;
   if (d_status && g_index_checks.load(std::memory_order_relaxed) &&
       (rc = launch_check_indices(end_pos, topk_idx, R, K, S_max, d_status, nullptr, stream)) != MLA_OK)
     return rc;
-  if ((rc = launch_absorb(q_nope, wkv_b, q_lat, R, d_status, stream, n_heads)) != MLA_OK) return rc;
+  if ((rc = launch_absorb(q_nope, wkv_b, q_lat, R, d_status, stream, n_heads, q_exp)) != MLA_OK) return rc;
   if ((rc = launch_attend_fp8(q_lat, q_pe, kv_fp8, pe, kv_scale, block_shift(block), cache_slot, end_pos, topk_idx,
                               scale, o_part, lse_part, R, K, S_max, n_slots, n_heads, n_split, span, wkv_b, d_status,
-                              stream, true)) != MLA_OK)
+                              stream, true, q_exp)) != MLA_OK)
     return rc;
   return launch_combine(o_part, lse_part, wkv_b, out, lse_out, R, n_split, d_status, stream, true, n_heads);
 }

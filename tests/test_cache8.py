@@ -341,6 +341,47 @@ def test_decode_matches_64_bits(R, h, K, S, block, slots):
     assert bool((lse[~some] == -math.inf).all()) and float((lse.double() - want_lse)[some].abs().max()) <= 1e-2
 
 
+@pytest.mark.parametrize("up", [-100, -30, 0, 30, 100])
+def test_decode_any_size_of_latent_query(up):
+    """W_UK and the rotary queries 2^up larger, the scale 2^-up: the same attention, whatever size the latent queries have; and
+    heads and 32-column chunks of very different sizes (absolute error of a score: of the largest chunk's)."""
+    g = gen(91)
+    R, h, K, S = 3, 70, 300, 400
+    c = make_cache(g, R, S, 4, loud=False)
+    qn, qp, w = decode_inputs(g, R, h)
+    wk = w.view(h, 256, 512).float()
+    wk[:, :128] *= torch.exp2(-torch.randint(0, 20, (h, 1, 16), generator=g, device=DEV).float()).repeat_interleave(32, 2)
+    wk[3, :128] = 0
+    end = torch.tensor([400, 257, 64], dtype=torch.int32, device=DEV)
+    idx = selection(g, end.tolist(), K, S)
+    plain = mla.mla_sparse_decode_fp8(qn, qp, c, end, idx, wk.to(bf).view(-1, 512), SCALE)
+    wk[:, :128] *= 2.0 ** up
+    out = mla.mla_sparse_decode_fp8(qn, (qp.float() * 2.0 ** up).to(bf), c, end, idx, wk.to(bf).view(-1, 512), SCALE * 2.0 ** -up)
+    want, _ = ref.decode(qn, (qp.float() * 2.0 ** up).to(bf), parts(c), torch.arange(R), end, idx, wk.to(bf).view(-1, 512), SCALE * 2.0 ** -up)
+    # 2^30 scales every factor exactly (the smallest weights are above 2^-30 2^-19 2^-5 2^-9 = 2^-63, the query's common power below
+    # 2^(8 + 30 + 5)): the same steps on the same digits.  2^-100 takes weights below bf16's 2^-126, which then have fewer digits.
+    assert abs(up) > 30 or torch.equal(out, plain)
+    assert float((out.double() - want).abs().max()) <= 1e-2 * float(want.abs().max()) + 1e-3
+
+
+def test_decode_infinite_weights_stay_in_their_head():
+    g = gen(92)
+    c = make_cache(g, 2, 90, 1)
+    qn, qp, w = decode_inputs(g, 2, 66)
+    end = torch.tensor([90, 90], dtype=torch.int32, device=DEV)
+    idx = selection(g, [90, 90], 80, 90)
+    want = mla.mla_sparse_decode_fp8(qn, qp, c, end, idx, w, SCALE)
+    bad = w.clone()
+    bad.view(66, 256, 512)[65, 5, 7] = math.inf
+    qn = qn.clone()
+    qn[0, 2, 9] = math.nan
+    out = mla.mla_sparse_decode_fp8(qn, qp, c, end, idx, bad, SCALE)
+    assert bool(torch.isnan(out[:, 65]).all()) and bool(torch.isnan(out[0, 2]).all())
+    out[:, 65], out[0, 2] = 0, 0
+    want[:, 65], want[0, 2] = 0, 0
+    torch.testing.assert_close(out.float(), want.float(), rtol=2.0 ** -6, atol=1e-3)  # without those heads, another common power
+
+
 def test_decode_graph_streams_and_repeats():
     """Captured and replayed on a side stream beside an eager call of other sizes; repeats are bit-identical."""
     g = gen(31)

@@ -68,8 +68,8 @@ def test_sizes(lib):
             for h in (1, 64, 65, 128):
                 n = lib.mla_num_splits_fp8(R, K, h)
                 assert 1 <= n <= min(128, -(-K // 128))
-                need = R * h * 512 * 2 + R * n * h * 512 * 2 + R * n * h * 4
-                assert need <= lib.mla_sparse_decode_fp8_workspace_size(R, K, 9000, h) <= need + 3 * 256
+                need = R * h * (512 * 2 + 4) + R * n * h * 512 * 2 + R * n * h * 4
+                assert need <= lib.mla_sparse_decode_fp8_workspace_size(R, K, 9000, h) <= need + 4 * 256
 
 
 def test_append(lib):
