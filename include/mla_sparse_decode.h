@@ -6,8 +6,11 @@
  * projection (mla_output_projection, mla_sparse_decode_project, page
  * "Attention update"), a tensor-parallel shard of both
  * (mla_sparse_decode_heads, mla_output_projection_shard), the fp8 weight
- * dequantisation (mla_dequant_fp8_blocks) and index validation
- * (mla_check_topk_indices).
+ * dequantisation (mla_dequant_fp8_blocks), index validation
+ * (mla_check_topk_indices), and an 8-bit latent cache: the call that writes it
+ * (mla_append_fp8), the decode step over it (mla_sparse_decode_fp8), and, for
+ * either cache, attention-weight totals (mla_accumulate_weights) and eviction
+ * by them (mla_evict).
  *
  * One decode step of DeepSeek-V3.2-Exp's absorbed multi-head latent attention
  * with the indexer's top-k mask, as the atlas pages of
@@ -451,13 +454,15 @@ int mla_output_projection_prepared(const void* x, const void* wo_prepared, void*
  *            [R,n_heads].  A call of at most 64 heads does half the attention
  *            work of one of 128
  *   workspace  mla_sparse_decode_fp8_workspace_size(R, K, S_max, n_heads)
- * The scores are exact to f32 accumulation (q_lat bf16); the softmax weights
- * enter the mix with 8 significant bits, as bf16 weights would, and the row
- * sums are f32.
+ * The latent queries enter the scores with nine significant bits and the
+ * rotary ones as given, the codes exactly; scores and row sums are f32.  The
+ * softmax weights enter the mix with eight significant bits, as bf16 weights
+ * would.  The queries of 64 heads (0 to 63, 64 to 127) share one power of two:
+ * what is 2^-18 of the largest of them is lost, and scores are that exact.
  *
  * mla_sparse_attend_fp8: steps "scores" .. "mix" alone, as mla_sparse_attend
  * (o_part bf16 [R,n_split,n_heads,512], lse_part f32 [R,n_split,n_heads];
- * q_lat bf16 [R,n_heads,512]); n_split must equal
+ * q_lat bf16 [R,n_heads,512], whose digits are all kept); n_split must equal
  * mla_num_splits_fp8(R, K, n_heads).
  * All return an mla_status; the size functions return 0 for invalid sizes.
  */
@@ -510,7 +515,9 @@ int mla_append_fp8(const void* kv_new, const void* pe_new, const int32_t* cu_row
  *   lse   f32 [B,n_heads], the decode step's lse_out
  *   acc   f32 [B,S_max], read and written at the selected positions only
  * A position's total gets one addition a call (valid indices are distinct), so
- * results are reproducible.  Scores and weights are f32.  Returns an mla_status.
+ * results are reproducible.  Scores and weights are f32, of the bf16 q_lat:
+ * weights of a row add up to the heads' number to within its rounding.  Returns
+ * an mla_status.
  */
 int mla_accumulate_weights(const void* q_lat, const void* q_pe, const void* kv_cache, const void* pe_cache,
                            const int32_t* end_pos, const int32_t* topk_idx, float scale, const float* lse, float* acc,

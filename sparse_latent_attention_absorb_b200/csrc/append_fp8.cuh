@@ -9,7 +9,9 @@
 // every step but the one rounding exact.
 //
 // Bound: HBM and, for a decode step's few rows, launch and load latency.  1152
-// bytes are read and 640 written a token.
+// bytes are read and 640 written a token.  Measured: 64 tokens 2.1 us, 2.9 where
+// 64 positions share a scale; 16K prompt tokens in blocks of 16 (29 MB) 9.8 us,
+// 3.0 TB/s, most of it the first loads' latency and the launch of 1100 CTAs.
 #pragma once
 
 #include <cuda_bf16.h>

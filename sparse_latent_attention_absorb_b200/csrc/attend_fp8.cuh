@@ -133,6 +133,19 @@ __device__ __forceinline__ uint32_t amax2(uint32_t m, uint32_t x) { return __vma
 // 64 (w / 4)..), 8-11 gather (one on each sub-partition of the SM: two warps on
 // two of them took 4900 cycles a tile), 12 query load and QK issue, 13 TMEM and PV
 // issue, 14 positions, scales and L2 prefetch, 15 pushes.
+//
+// Measured (one B200, 64 rows of 2048 positions, 128 heads): 49 us, of which 10
+// lie before the first and behind the last tile (set-up 1.5, the query 0.6 and
+// its limbs 2.5, the last tile's way to O 1.5, O to memory 1.9) and 2.4 us, 4500
+// cycles, are a tile's.  A tile's limits are 2340 cycles of MMA, about 2800 of
+// shared-memory traffic (the MMAs' operands, the copies, P) and 2850 of gather
+// from HBM (1290 from L2); what sets the pace is the chain of hand-overs between
+// them, each of a few hundred cycles: without the softmax's arithmetic a tile
+// takes 5% less, with half the MMAs 7%, with the peer's columns not copied 8%,
+// with all three 22%.  Slower: MMAs over both CTAs (cta_group::2, M = 256, N =
+// 128, no pushes: 135 cycles an MMA, 59.6 us), two full sets of P and two stages
+// (59), one set of P and a ring of four (53.3), PV behind the next QK but one
+// (58.5), the L2 prefetch in bulk (59.7) or none (50.0).
 // =============================================================================
 constexpr int kF8Heads = 64;           // heads of a CTA's QK and softmax
 constexpr int kF8Nt = 128;             // positions of a tile

@@ -13,7 +13,7 @@
 // rows a cluster of eight: 64 rows of 8192 take about 13 us, 27000 cycles of
 // which 6300 are the first read of the totals and their histogram, 4600 the
 // numbering), the move by HBM (64 rows of up to 8192 keeping 2500 in 8 bits, 209 MB:
-// 38 us, 5.5 TB/s).  The move's CTAs come up while the selection runs.
+// 35 us, 6.0 TB/s).  The move's CTAs come up while the selection runs.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -242,15 +242,19 @@ evict_select_kernel(const float* acc, const int32_t* __restrict__ end_pos, float
   for (int i = n_new + tid; i < S_max; i += kSelectThreads) out[i] = 0.f;
 }
 
-// Rows kept[i] of a slot to rows i, 128 a step: 16 warps of eight rows, held in
+// Rows kept[i] of a slot to rows i: 16 warps of eight rows (four), held in
 // registers.  The 8-bit cache's new blocks get the largest scale of their rows,
 // and rows of a smaller one are rounded again.
-//   out of place: a CTA per 128 rows;
+//   out of place: a CTA per 128 (64) rows;
 //   in place: a cluster of eight CTAs per slot walks up its rows, and writes a
 //   step once all of it has been read (kept[i] >= i: what a step writes, no
 //   later step reads).
 constexpr int kMoveThreads = 512;
-constexpr int kMoveRows = 128;
+// Rows of a warp, and of a CTA: out of place two CTAs share an SM, so that one
+// reads while the other writes, and bf16 rows then leave registers for four a
+// warp.  (A CTA's 128 rows of the 8-bit cache are whole blocks of positions.)
+__host__ __device__ constexpr int move_warp_rows(bool fp8, bool in_place) { return fp8 || in_place ? 8 : 4; }
+__host__ __device__ constexpr int move_rows(bool fp8, bool in_place) { return kMoveThreads / 32 * move_warp_rows(fp8, in_place); }
 constexpr int kMoveCluster = 8;
 
 struct MoveArgs {
@@ -267,9 +271,10 @@ struct MoveArgs {
 };
 
 template <bool kFp8, bool kInPlace>
-__global__ void __launch_bounds__(kMoveThreads, 1) evict_move_kernel(const MoveArgs a) {
+__global__ void __launch_bounds__(kMoveThreads, kInPlace ? 1 : 2) evict_move_kernel(const MoveArgs a) {
   constexpr int kVecs = kFp8 ? 1 : 2;  // 16-byte pieces of a lane
   constexpr size_t kRow = kVecs * 512;
+  constexpr int kWarpRows = move_warp_rows(kFp8, kInPlace), kMoveRows = move_rows(kFp8, kInPlace);
   __shared__ float src_scale[kMoveRows], dst_scale[kMoveRows];
   const int b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   grid_dep_wait();  // kept and new_end come from the selection
@@ -285,12 +290,12 @@ __global__ void __launch_bounds__(kMoveThreads, 1) evict_move_kernel(const MoveA
       const int last = min(base + step, n) - 1;
       if (kept[last] == last) continue;  // nothing has moved up to here
     }
-    int src[8];
-    uint4 v[8][kVecs];
-    uint32_t pe[8];
+    int src[kWarpRows];
+    uint4 v[kWarpRows][kVecs];
+    uint32_t pe[kWarpRows];
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      const int i = i0 + 8 * warp + r;
+    for (int r = 0; r < kWarpRows; ++r) {
+      const int i = i0 + kWarpRows * warp + r;
       src[r] = i < n ? kept[i] : -1;
     }
     if (kFp8 && tid < kMoveRows) {
@@ -298,7 +303,7 @@ __global__ void __launch_bounds__(kMoveThreads, 1) evict_move_kernel(const MoveA
       src_scale[tid] = s >= 0 ? a.scale[(size_t)b * a.n_blocks + (s >> a.shift)] : 0.f;
     }
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
+    for (int r = 0; r < kWarpRows; ++r) {
       if (src[r] < 0) continue;
       const size_t at = row0 + src[r];
 #pragma unroll
@@ -307,10 +312,9 @@ __global__ void __launch_bounds__(kMoveThreads, 1) evict_move_kernel(const MoveA
     }
     __syncthreads();
     if (kFp8 && tid < kMoveRows) {
-      // the block's largest scale (a tile holds whole blocks)
-      const int t0 = tid & ~(block - 1);
-      float s = src_scale[t0];
-      for (int t = t0 + 1; t < t0 + block; ++t) s = fmaxf(s, src_scale[t]);
+      // the block's largest scale, of 32 rows at most
+      float s = src_scale[tid];
+      for (int o = 1; o < min(block, 32); o <<= 1) s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, o));
       dst_scale[tid] = s;
     }
     if (kInPlace) {
@@ -318,14 +322,19 @@ __global__ void __launch_bounds__(kMoveThreads, 1) evict_move_kernel(const MoveA
     } else {
       __syncthreads();
     }
+    auto block_scale = [&](int t) {  // (a tile holds whole blocks)
+      float s = dst_scale[t];
+      for (int o = 32; o < block; o += 32) s = fmaxf(s, dst_scale[(t & ~(block - 1)) | ((t + o) & (block - 1))]);
+      return s;
+    };
     if (kFp8 && tid < kMoveRows && i0 + tid < n && (tid & (block - 1)) == 0)
-      a.scale_out[(size_t)b * a.n_blocks + ((i0 + tid) >> a.shift)] = dst_scale[tid];
+      a.scale_out[(size_t)b * a.n_blocks + ((i0 + tid) >> a.shift)] = block_scale(tid);
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
+    for (int r = 0; r < kWarpRows; ++r) {
       if (src[r] < 0) continue;
-      const size_t at = row0 + i0 + 8 * warp + r;
+      const size_t at = row0 + i0 + kWarpRows * warp + r;
       if (kFp8) {
-        const float from = src_scale[8 * warp + r], to = dst_scale[8 * warp + r];
+        const float from = src_scale[kWarpRows * warp + r], to = block_scale(kWarpRows * warp + r);
         if (from != to) {
           v[r][0] = recode16(v[r][0], from / to);
           pe[r] = rescale_pe(pe[r], from / to);

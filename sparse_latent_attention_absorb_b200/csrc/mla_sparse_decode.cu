@@ -838,7 +838,7 @@ int run_evict(const EvictBuffers& e, const int32_t* end_pos, int32_t* kept, int3
   if (in_place)
     return launch_cluster(evict_move_kernel<kFp8, true>, kMoveCluster, dim3(kMoveCluster, (unsigned)B),
                           dim3(kMoveThreads), 0, stream, true, a);
-  return launch_ex(evict_move_kernel<kFp8, false>, dim3((unsigned)ceil_div(keep, kMoveRows), (unsigned)B),
+  return launch_ex(evict_move_kernel<kFp8, false>, dim3((unsigned)ceil_div(keep, move_rows(kFp8, false)), (unsigned)B),
                    dim3(kMoveThreads), 0, stream, true, a);
 }
 constexpr int kMaxEvictRows = 65535;  // grid y

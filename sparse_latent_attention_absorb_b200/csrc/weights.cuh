@@ -44,11 +44,14 @@ __device__ __forceinline__ float sum_transposed(float (&v)[32], int lane) {
 // Bound: the gather, 1152 (640) bytes a position, each read once.  The rows
 // come in groups of blocks (16 KB: 128 positions x 128 bytes): a group is
 // awaited, multiplied and released as one, since a wait and its proxy fence
-// cost as much as a block's MMAs.
+// cost as much as a block's MMAs.  Measured: 64 rows of 2048 positions in bf16
+// (162 MB) 32.9 us, 4.9 TB/s; 8 rows in 8 bits 11.3 us, most of it the query's
+// way into TMEM.  An L2 prefetch of the next tile's rows held up the copies in
+// the load pipeline (43 us); eight gather warps change nothing.
 //
 // Warps (448 threads): 0-7 weights (warp w: heads 32 (w % 4).., positions
-// 64 (w / 4)..), 8-11 gather, 12 TMEM, query load and QK issue, 13 positions,
-// scales and L2 prefetch.
+// 64 (w / 4)..), 8-11 gather, 12 TMEM, query load and QK issue, 13 positions and
+// scales.
 // =============================================================================
 constexpr int kWtNt = 128;
 constexpr int kWtBlock = kWtNt * 128;
