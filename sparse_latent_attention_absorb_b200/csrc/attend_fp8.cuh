@@ -647,12 +647,15 @@ sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const uint8_t
         for (int q = 0; q < 4; ++q) v[q] = piece(8 * c4 + 2 * q + (hi_row ? 0 : 1));
         // as fp16 numbers 2^(e - 8) x
         if (scaled) {
-          const __half2 to = half2_power((c4 < 2 ? ex[0] : ex[1]) + e - 8);
+          auto times = [&](int x) {
+            const __half2 to = half2_power(x);
+            auto one = [&](uint32_t h) { return half2_bits(__hmul2(*reinterpret_cast<const __half2*>(&h), to)); };
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            auto times = [&](uint32_t h) { return half2_bits(__hmul2(*reinterpret_cast<const __half2*>(&h), to)); };
-            v[q] = make_uint4(times(v[q].x), times(v[q].y), times(v[q].z), times(v[q].w));
-          }
+            for (int q = 0; q < 4; ++q) v[q] = make_uint4(one(v[q].x), one(v[q].y), one(v[q].z), one(v[q].w));
+          };
+          const int x = (c4 < 2 ? ex[0] : ex[1]) + e - 8, x1 = min(max(x, -14), 15);
+          times(x1);
+          if (__any_sync(0xffffffffu, x != x1)) times(x - x1);  // a chunk far from its bound, or from the largest
         } else {
           const float to = mul * (1.f / 256.f);
 #pragma unroll

@@ -266,7 +266,6 @@ struct MoveArgs {
   float* scale_out;
   const int32_t* kept;     // [B, keep]
   const int32_t* new_end;  // [B]
-  const int32_t* end_pos;  // [B]
   int S_max, keep, shift, n_blocks;
 };
 

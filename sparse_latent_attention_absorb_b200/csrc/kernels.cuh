@@ -86,9 +86,9 @@ __device__ unsigned long long g_mla_kernel_ns[kKernelEvents];
 // together (rounded to bf16's eight it would be the largest error of that decode
 // step).  The power comes from a bound that costs no look at the results, |q_lat|
 // <= 128 max|q_nope[b,h]| max|W_UK[h, :, chunk]| (of the row itself and of the
-// weights: rows stay independent), which fp16 sees below 2^4; a result 2^12 below
-// its bound still keeps bf16's digits.  q_exp [n_heads, 4, B]: result = fp16
-// 2^(127 - q_exp).
+// weights: rows stay independent), which fp16 sees below 2^15.  The largest
+// results are usually 2^6 below their bound; one 2^22 below it still has bf16's
+// digits.  q_exp [n_heads, 4, B]: result = fp16 2^(127 - q_exp).
 template <bool kScaled>
 __global__ void __launch_bounds__(128, 1)
 absorb_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_q,
@@ -178,7 +178,7 @@ absorb_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ 
     const uint32_t q = tid < n_tile ? top(sB + tid * 128, n_tile * 128) : 0u;
     __syncthreads();
     const int e_w = (int)max(max(top_w[0], top_w[1]), max(top_w[2], top_w[3]));
-    const int up = min(max(249 - (int)q - e_w, -126), 126);
+    const int up = min(max(260 - (int)q - e_w, -126), 126);
     if (tid < n_tile) {
       row_scale[tid] = __uint_as_float((uint32_t)(127 + up) << 23);
       if (b0 + tid < B) q_exp[(size_t)(h * (kDl / 128) + chunk) * B + b0 + tid] = (uint8_t)(127 + up);

@@ -823,10 +823,12 @@ int run_evict(const EvictBuffers& e, const int32_t* end_pos, int32_t* kept, int3
   DeviceInfo* info = nullptr;
   int rc = prepare(&info);
   if (rc != MLA_OK) return rc;
-  // Eight CTAs a row where its positions outweigh their meetings: 32K positions
-  // of 8 rows 18 us against 42, of 16 rows 33 against 42, of 32 rows 47 against
-  // 42 (their clusters no longer fit at once); 8K of 8 rows 17.6 against 18.7.
-  const int n_cta = B <= 16 && S_max > (B <= 8 ? 8192 : 16384) ? kSelectCluster : 1;
+  // Eight CTAs a row where its positions outweigh their meetings and all
+  // clusters run at once.  Whole calls that keep 64 positions, eight CTAs a row
+  // against one: 1 row of 4K 14.4 us and 13.4, of 8K 15.3 and 17.9; 8 rows of 8K
+  // 15.3 and 18.1, of 32K 18.4 and 49.6; 16 rows of 8K 26.9 and 17.5, of 16K 29.3
+  // and 29.4, of 32K 33.1 and 49.4; 32 rows of 32K (two rounds) 48.0 and 49.4.
+  const int n_cta = B <= info->sm_count / kSelectCluster && S_max >= (B <= 8 ? 8192 : 16385) ? kSelectCluster : 1;
   if ((rc = launch_cluster(evict_select_kernel, (unsigned)n_cta, dim3((unsigned)(B * n_cta)), dim3(kSelectThreads), 0, stream, false,
                       static_cast<const float*>(e.in[0]), end_pos, static_cast<float*>(e.out[0]), kept, new_end, S_max,
                       keep, recent)) != MLA_OK)
@@ -834,7 +836,7 @@ int run_evict(const EvictBuffers& e, const int32_t* end_pos, int32_t* kept, int3
   const MoveArgs a{static_cast<const uint8_t*>(e.in[1]), static_cast<const uint8_t*>(e.in[2]),
                    kFp8 ? static_cast<const float*>(e.in[3]) : nullptr, static_cast<uint8_t*>(e.out[1]),
                    static_cast<uint8_t*>(e.out[2]), kFp8 ? static_cast<float*>(e.out[3]) : nullptr, kept, new_end,
-                   end_pos, S_max, keep, shift, ((S_max - 1) >> shift) + 1};
+                   S_max, keep, shift, ((S_max - 1) >> shift) + 1};
   if (in_place)
     return launch_cluster(evict_move_kernel<kFp8, true>, kMoveCluster, dim3(kMoveCluster, (unsigned)B),
                           dim3(kMoveThreads), 0, stream, true, a);

@@ -364,6 +364,27 @@ def test_decode_any_size_of_latent_query(up):
     assert float((out.double() - want).abs().max()) <= 1e-2 * float(want.abs().max()) + 1e-3
 
 
+@pytest.mark.parametrize("big", [2.0 ** 10, 2.0 ** 20])
+def test_decode_large_factors_that_meet_no_weight(big):
+    """Query columns far larger than the others whose weights are zero, in some heads, change nothing: bounds on the latent queries
+    that are 2^17 and 2^27 too large."""
+    g = gen(93)
+    c = make_cache(g, 2, 200, 8)
+    qn, qp, w = decode_inputs(g, 2, 70)
+    wk = w.view(70, 256, 512).clone()
+    wk[::3, 5] = 0
+    quiet, loud = qn.clone(), qn.clone()
+    quiet[:, ::3, 5], loud[:, ::3, 5] = 0, big
+    end = torch.tensor([200, 77], dtype=torch.int32, device=DEV)
+    idx = selection(g, [200, 77], 150, 200)
+    a, b = (mla.mla_sparse_decode_fp8(q, qp, c, end, idx, wk.view(-1, 512), SCALE) for q in (quiet, loud))
+    # fp16 below its normal numbers at worst: 2^-25 in units that put the bound, 2^7 big times the usual size, at 2^15: 2^-13 of the
+    # usual size at 2^20, less than the 2^-9 that a bf16 query would be off
+    torch.testing.assert_close(b.float(), a.float(), rtol=2.0 ** -6, atol=4e-3 * float(a.float().abs().max()))
+    want, _ = ref.decode(loud, qp, parts(c), torch.arange(2), end, idx, wk.view(-1, 512), SCALE)
+    assert float((b.double() - want).abs().max()) <= 1e-2 * float(want.abs().max()) + 1e-3
+
+
 def test_decode_infinite_weights_stay_in_their_head():
     g = gen(92)
     c = make_cache(g, 2, 90, 1)
