@@ -458,7 +458,8 @@ int mla_output_projection_prepared(const void* x, const void* wo_prepared, void*
  * rotary ones as given, the codes exactly; scores and row sums are f32.  The
  * softmax weights enter the mix with eight significant bits, as bf16 weights
  * would.  The queries of 64 heads (0 to 63, 64 to 127) share one power of two:
- * what is 2^-18 of the largest of them is lost, and scores are that exact.
+ * what is 2^-18 of the largest of them (or 2^-70 of the largest rotary factor)
+ * is lost, and scores are that exact.
  *
  * mla_sparse_attend_fp8: steps "scores" .. "mix" alone, as mla_sparse_attend
  * (o_part bf16 [R,n_split,n_heads,512], lse_part f32 [R,n_split,n_heads];

@@ -91,6 +91,26 @@ __device__ __forceinline__ __half2 half2_power(int x) {
 // The magnitudes' bits of two bf16 numbers, each the larger of m's and x's.
 __device__ __forceinline__ uint32_t amax2(uint32_t m, uint32_t x) { return __vmaxu2(m, x & 0x7fff7fffu); }
 
+// The largest finite magnitude of a thread's 32 rotary factors (one that holds an
+// infinity or NaN counts none: its head's scores are NaN anyway).
+__device__ __forceinline__ float rotary_top(const uint4 (&r)[4]) {
+  uint32_t m2 = 0;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) m2 = amax2(amax2(amax2(amax2(m2, r[u].x), r[u].y), r[u].z), r[u].w);
+  const uint32_t m = max(m2 & 0xffffu, m2 >> 16);
+  return m < 0x7f80u ? __uint_as_float(m << 16) : 0.f;
+}
+// The common exponent of queries up to `amax` and rotary ones up to `rmax`, which
+// go along as 2^e q_pe: these stay below 2^60, so that no sum of theirs overflows
+// where the others are far smaller.
+__device__ __forceinline__ int query_exponent(float amax, float rmax) {
+  const int e = limb_exponent(amax);
+  if (!(rmax > 0.f)) return e;
+  int k;
+  frexpf(rmax, &k);  // rmax < 2^k
+  return min(e, 60 - k);
+}
+
 // =============================================================================
 // sparse_attend_fp8_kernel
 //
@@ -599,6 +619,8 @@ sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const uint8_t
         }
       }
 
+      const float rtop = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(rotary_top(r4))));
+
       wait(smem_u32(&bars->q_tma), 0, ab);
       float top = 0.f;
       bool finite = true;
@@ -619,13 +641,13 @@ sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const uint8_t
         top = 0.f;
       }
       top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-      if (lane == 0) red[warp] = top;
+      if (lane == 0) red[warp] = top, red[kF8SoftmaxWarps + warp] = rtop;
       named_bar_sync(1, kSoftmaxThreads);
       bad = fin[hd] != 0.f;
-      float am = red[0];
+      float am = red[0], rm = red[kF8SoftmaxWarps];
 #pragma unroll
-      for (int w = 1; w < kF8SoftmaxWarps; ++w) am = fmaxf(am, red[w]);
-      const int e = limb_exponent(am);
+      for (int w = 1; w < kF8SoftmaxWarps; ++w) am = fmaxf(am, red[w]), rm = fmaxf(rm, red[kF8SoftmaxWarps + w]);
+      const int e = query_exponent(am, rm);
       const float mul = exp2_int(e);
       c2 = scale * 1.4426950408889634f * exp2_int(-e);
 #pragma unroll

@@ -276,6 +276,7 @@ accumulate_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __nv_b
       const uint4* psrc = reinterpret_cast<const uint4*>(q_pe + ((size_t)b * n_heads + (live ? hd : 0)) * kDr) + 4 * ch;
 #pragma unroll
       for (int u = 0; u < 4; ++u) r4[u] = live ? __ldg(psrc + u) : make_uint4(0, 0, 0, 0);
+      const float rtop = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(rotary_top(r4))));
       wait(smem_u32(&bars->q_tma), 0, ab);
       float mul = 1.f;
       if (kFp8) {
@@ -291,12 +292,12 @@ accumulate_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __nv_b
           m = 0;
         }
         m = __reduce_max_sync(0xffffffffu, m);
-        if (lane == 0) red[warp] = __uint_as_float(m << 16);
+        if (lane == 0) red[warp] = __uint_as_float(m << 16), red[8 + warp] = rtop;
         named_bar_sync(1, 256);
-        float am = red[0];
+        float am = red[0], rm = red[8];
 #pragma unroll
-        for (int w = 1; w < 8; ++w) am = fmaxf(am, red[w]);
-        const int e = limb_exponent(am);
+        for (int w = 1; w < 8; ++w) am = fmaxf(am, red[w]), rm = fmaxf(rm, red[8 + w]);
+        const int e = query_exponent(am, rm);
         mul = exp2_int(e);
         c2 *= exp2_int(-e);
         if (bad_s[hd] != 0.f) c2 = __int_as_float(0x7fffffff);

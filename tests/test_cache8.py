@@ -265,6 +265,24 @@ def test_attend_scores_that_move_along_the_tiles(h, up):
     check_attend(q_lat, q_pe, c, end, idx, None)
 
 
+@pytest.mark.parametrize("h", [128, 20])
+@pytest.mark.parametrize("size", [2.0 ** -115, 2.0 ** -60])
+def test_attend_latent_queries_far_below_the_rotary_ones(h, size):
+    """The common power that would lift such queries would lift the rotary ones out of f32's range; totals too."""
+    g = gen(57)
+    c = make_cache(g, 2, 300, 4)
+    q_lat = (torch.randn(2, h, 512, generator=g, device=DEV) * size).to(bf)
+    q_pe = (torch.randn(2, h, 64, generator=g, device=DEV) * 100).to(bf)
+    end = torch.tensor([300, 140], dtype=torch.int32, device=DEV)
+    idx = selection(g, [300, 140], 200, 300)
+    check_attend(q_lat, q_pe, c, end, idx, None)
+    lse = torch.stack([ref.attend(q_lat[b], q_pe[b], parts(c), b, ref.selected(idx[b], end[b], 300), SCALE)[2] for b in range(2)]).float()
+    acc = mla.mla_accumulate_weights_fp8(q_lat, q_pe, c, end, idx, SCALE, lse, torch.zeros(2, 300, device=DEV))
+    # a row's weights add up to the heads; scores are f32 sums of 576 products, each off by 2^-24 of what it has reached, exp by as much
+    size = float(lse.abs().max()) + 1
+    assert float((acc.sum(1) - h).abs().max()) <= h * 640 * 2.0 ** -23 * size
+
+
 def test_attend_reads_only_the_selected_rows():
     g = gen(21)
     c = make_cache(g, 2, 600, 1)
