@@ -20,11 +20,11 @@
 namespace mla {
 
 // ---------------------------------------------------------------- E4M3 limbs
-// A factor kept as two E4M3 numbers has 8 significant bits, bf16's own count,
-// and 8-bit products run at twice the rate of bf16 products: two of them cost
-// what one bf16 product costs, and the codes go to the tensor cores as they
-// lie in the cache, with no conversion and at half of bf16's shared memory.
-
+// A factor kept as two E4M3 numbers has nine significant bits (four, four and
+// the second's sign), one more than bf16's, and 8-bit products run at twice the
+// rate of bf16 products: two of them cost what one bf16 product costs, and the
+// codes go to the tensor cores as they lie in the cache, with no conversion and
+// at half of bf16's shared memory.
 //
 // An fp16 number f of magnitude below 1.8 has E4M3's exponent field for the
 // value 2^8 f, subnormals included, so rounding 2^8 f to E4M3 is rounding f's
