@@ -178,7 +178,8 @@ def test_a_serving_loop(block):
         assert float((lse.double() - want_lse).abs().max()) <= 1e-2
         before = acc.sum(1)
         mla.mla_accumulate_weights_fp8(mla.mla_absorb_q(qn, w), qp, c, end, idx, SCALE, lse, acc)
-        # every head's weights sum to one: 2^-20 a weight, its share of the total's rounding
+        # every head's weights sum to one, to a weight's 2^-20 and what the totals' bf16 q_lat moves a score by: 0.072 * 0.5 * 2^-9 *
+        # sqrt(512) = 1.6e-3 for one, of either sign, over 128 heads and 200 positions
         torch.testing.assert_close(acc.sum(1) - before, torch.full((B,), 128.0, device=DEV), rtol=1e-3, atol=0)
         if step == 2:
             kept, end = run(c, acc, end, 150, 30, in_place=True)
