@@ -457,7 +457,10 @@ int mla_output_projection_prepared(const void* x, const void* wo_prepared, void*
  * The latent queries enter the scores with nine significant bits and the
  * rotary ones as given, the codes exactly; scores and row sums are f32.  The
  * softmax weights enter the mix with eight significant bits, as bf16 weights
- * would.  The queries of 64 heads (0 to 63, 64 to 127) share one power of two:
+ * would, where weight times scale is at least 2^-7 of the largest of the same
+ * 128 index slots; what is smaller is off by at most 2^-15 of that one or, if it
+ * is more, of the mean of the sums of the 128-slot tiles so far (a tile's 128
+ * together by 2^-8 of it).  The queries of 64 heads (0 to 63, 64 to 127) share one power of two:
  * what is 2^-18 of the largest of them (or 2^-70 of the largest rotary factor)
  * is lost, and scores are that exact.
  *

@@ -47,6 +47,12 @@ __device__ __forceinline__ uint32_t limb_bytes_positive(uint32_t a, uint32_t b) 
   return __byte_perm(a << 1, b << 1, 0x7531);
 }
 __device__ __forceinline__ uint32_t half2_bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
+// The E5M2 bytes of 2^8 times four fp16 numbers (below 2^7): an E5M2 number is
+// the upper byte of an fp16 one.  Ties go away from zero.
+__device__ __forceinline__ uint32_t limb_bytes_e5m2(__half2 a, __half2 b) {
+  const __half2 up = __float2half2_rn(256.f);
+  return __byte_perm(half2_bits(__hmul2(a, up)) + 0x00800080u, half2_bits(__hmul2(b, up)) + 0x00800080u, 0x7531);
+}
 
 // Exponent e with |amax| 2^e in (224, 448] (0 for amax = 0).
 __device__ __forceinline__ int limb_exponent(float amax) {
@@ -138,9 +144,10 @@ __device__ __forceinline__ int query_exponent(float amax, float rmax) {
 // Single (at most 64 heads): one CTA per (row, split) owns all 512 columns.
 //
 // m_h is the largest y of some tile plus a margin, and moves only when P would
-// leave E4M3's range; the softmax warps then rescale the columns of O of the
-// heads it moved for between two PVs, in both CTAs of a pair (which tell each
-// other as soon as they know; P does not wait for that, only PV does).
+// leave E4M3's range or lose its small weights; the softmax warps then rescale
+// the columns of O of the heads it moved for between two PVs, in both CTAs of a
+// pair (which tell each other as soon as they know; P does not wait for that,
+// only PV does).
 //
 // Shared memory: blocks of 16 KB (128 positions x 128 bytes, 128-byte swizzle).
 //   Pair:   three for what only QK reads (rotary rows, the peer's columns),
@@ -185,8 +192,8 @@ __host__ __device__ constexpr int f8_p_at(bool pair, int j, int lo) {
 constexpr int kF8OffQpe = 12 * kF8Block;                     // 128 rows (the lo rows are zero)
 constexpr int kF8OffKey = kF8OffQpe + kF8Block;              // f32 [4][3][128]: what a position's scale enters by
 constexpr int kF8OffPos = kF8OffKey + 4 * 3 * kF8Nt * 4;     // int [4][128]: a tile's positions, -1 = masked
-constexpr int kF8OffRed = kF8OffPos + 4 * kF8Nt * 4;         // f32 [2][2][64]
-constexpr int kF8OffMove = kF8OffRed + 2 * 2 * kF8Heads * 4; // F8Move [2][2]
+constexpr int kF8OffRed = kF8OffPos + 4 * kF8Nt * 4;         // f32 [4][2][64]
+constexpr int kF8OffMove = kF8OffRed + 4 * 2 * kF8Heads * 4; // F8Move [2][2]
 constexpr int kF8OffFin = kF8OffMove + 2 * 2 * 272;          // f32 [128]: one over the row sums
 constexpr int kF8OffBar = kF8OffFin + kH * 4;
 constexpr int kF8SmemBytes = kF8OffBar + 512 + kSmemAlignPad;
@@ -196,15 +203,29 @@ constexpr int kF8Threads = 512;
 constexpr uint32_t kF8ColS = 0;    // scores: 128 columns
 constexpr uint32_t kF8ColQ = 128;  // the query's limbs: 128 columns of four codes
 constexpr uint32_t kF8ColO = 256;  // pair: 2 blocks of 128 heads; single: 4 blocks of 64
-// P is formed in fp16 at 2^-8 of its E4M3 value.  A new m_h puts the largest P
-// of its tile at 2^3 (in E4M3); a later one may reach 2^8.75 = 430 (E4M3's
-// largest value is 448) before m_h has to move.  E4M3 resolves 2^-9: more room
-// above costs small weights their bits (the mix of 2048 positions of
-// unit-variance scores is off by 5.8e-4 at 2^5, 8.0e-4 at 2^3, 1.3e-3 at 2^2),
-// less of it moves m_h more often (13, none and none of 15 tiles had a head
-// that moved, at 2^5, 2^3 and 2^2).
-constexpr float kF8RefMargin = 8.0f - 3.0f;
+// P is formed in fp16 at 2^-8 of what the products see; the powers below are
+// theirs.  Its first limb is E4M3, its second what that leaves, as E5M2: 2^-4 of
+// 2^-4, eight significant bits like bf16's, down to P = 2^-6.  A smaller P keeps
+// fewer (E4M3 steps by 2^-9 there, E5M2 has three bits of the rest): it is off by
+// 2^-14 at most.  Over a tile that may add up to 2^-7, so it has to be little
+// beside what the head has:
+//   a new m_h puts the largest P of its tile at 2^2, and a later one may reach
+//   2^8.75 = 430 (E4M3's largest value is 448) before m_h has to rise;
+//   m_h falls again where a tile's largest is below 2^1 and the sum of P over the
+//   j tiles before it below 2^1 (j + 1): a tile that keeps its m_h is then off by
+//   2^-8 of its largest weight or of the mean of the tiles' sums at most.
+// m_h falls no further than 2^-32 of the largest weight so far.  A second limb in
+// E4M3, with references that only rise, loses all weights below 2^-13 of the
+// largest: beside one of 0.8 of the softmax the mix of 2048 positions is off by
+// 3.2e-2, of 8192 by 1.0e-1, against 2e-4 and 8e-5 so (bf16 weights 8e-4; a
+// restatement on the CPU).  Measured, 64 rows of 2048 positions whose scales
+// differ by factors of four: 50.7 us, 49.6 without falling references; new ones
+// at 2^3 51.4, at 2^4 52.8 (they fall and rise more often).
+constexpr float kF8RefMargin = 8.0f - 2.0f;
 constexpr float kF8RefLimit = 8.75f - 8.0f;
+constexpr float kF8RefFloor = 1.0f - 8.0f;
+constexpr float kF8MassFloor = 1.f / 128.f;  // 2^kF8RefFloor
+constexpr float kF8RefFall = 32.f;
 constexpr float kF8NoRef = -1e30f;  // m_h before any position counted
 // How a tile moves the references of a CTA's 64 heads.
 struct F8Move {
@@ -284,7 +305,7 @@ sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const uint8_t
 
   const uint32_t s0 = smem_u32(smem);
   float* key = reinterpret_cast<float*>(smem + kF8OffKey);      // [tile & 3][s | log2 s | 1/s][128]
-  float* red = reinterpret_cast<float*>(smem + kF8OffRed);      // [tile & 1][position half][head]
+  float* red = reinterpret_cast<float*>(smem + kF8OffRed);      // tops, then sums: [tile & 1][position half][head]
   int* pos_s = reinterpret_cast<int*>(smem + kF8OffPos);        // [tile & 3][128]
   F8Move* moves = reinterpret_cast<F8Move*>(smem + kF8OffMove);  // [tile & 1][rank]
   float* fin = reinterpret_cast<float*>(smem + kF8OffFin);
@@ -537,7 +558,7 @@ sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const uint8_t
   } else if (warp == kF8PvWarp) {
     // ------------------------------------------------ PV issue
     if (lane == 0) {
-      constexpr uint32_t id_pv = idesc_e4m3_f32(128, kCols, true, false);
+      constexpr uint32_t id_hi = idesc_e4m3_f32(128, kCols, true, false), id_lo = id_hi | kIdescBE5m2;
       const uint64_t d_0 = smem_desc_sw128(s0, 16, 1024);
       int st = 0;
       for (int j = 0; j < n_tiles; ++j) {
@@ -554,15 +575,15 @@ sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const uint8_t
         // on their way.
         const uint64_t v0 = d_0 + (uint64_t)((f8_own_at(kPair, 0, 0) + st * (kOwn * kF8Block)) >> 4);
         const uint64_t p_hi = d_0 + (uint64_t)(f8_p_at(kPair, j, 0) >> 4), p_lo = d_0 + (uint64_t)(f8_p_at(kPair, j, 1) >> 4);
-        auto pv = [&](int m, int k, uint64_t p, bool first) {
+        auto pv = [&](int m, int k, uint64_t p, uint32_t id, bool first) {
           mma_f8_ss(tmem + kF8ColO + m * kCols, v0 + (uint64_t)((m * kF8Block + k * 32 * 128) >> 4), p + (uint64_t)((k * 32) >> 4),
-                    id_pv, first ? 0u : 1u);
+                    id, first ? 0u : 1u);
         };
         if (kPair) {
 #pragma unroll 1
           for (int m = 0; m < kOwn; ++m)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) pv(m, k, p_hi, j == 0 && k == 0);
+            for (int k = 0; k < 4; ++k) pv(m, k, p_hi, id_hi, j == 0 && k == 0);
           mma_commit_to(smem_u32(&bars->hi_free), (uint16_t)3);
           if (wait_cluster(smem_u32(&bars->p_lo[pb]), ph, ab) && j + 2 < n_tiles)
             mbar_arrive_expect_tx(smem_u32(&bars->p_lo[pb]), kF8Limb);
@@ -571,8 +592,8 @@ sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const uint8_t
         for (int m = 0; m < kOwn; ++m)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            if (!kPair) pv(m, k, p_hi, j == 0 && k == 0);
-            pv(m, k, p_lo, false);
+            if (!kPair) pv(m, k, p_hi, id_hi, j == 0 && k == 0);
+            pv(m, k, p_lo, id_lo, false);
           }
         mma_commit(smem_u32(&bars->own_empty[st]));
         mma_commit(smem_u32(&bars->tile_done[j & 3]));
@@ -717,7 +738,10 @@ sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const uint8_t
     if (bad) c2 = __int_as_float(0x7fffffff);
     const float w_k = hi_row ? c2 : c2 * kLimbLo, w_r = hi_row ? c2 * kLimbLo : c2;
     const uint64_t w_keep = pack_f32x2(w_k, w_k), w_recv = pack_f32x2(w_r, w_r);
-    float m_ref = kF8NoRef, l = 0.f;
+    // l: the row sum; mass: the sum of P (fp16's range, which is enough to choose
+    // m_h by); both of the thread's positions
+    float m_ref = kF8NoRef, peak = -INFINITY, l = 0.f, mass = 0.f;
+    if (hi_row) red[(4 + ch) * kF8Heads + hd] = 0.f;
     for (int j = 0; j < n_tiles; ++j) {
       const ulonglong2* kt = reinterpret_cast<const ulonglong2*>(key + (j & 3) * (3 * kF8Nt) + first);
       F8Move* mv = moves + 2 * (j & 1) + rank;  // tile j - 2's is done: its PVs are
@@ -761,9 +785,13 @@ sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const uint8_t
       if (hi_row) rt[ch * kF8Heads + hd] = top;
       named_bar_sync(2 + qd, 64);
       top = fmaxf(top, rt[(ch ^ 1) * kF8Heads + hd]);
+      const float sums = rt[4 * kF8Heads + hd] + rt[5 * kF8Heads + hd];
 
-      const bool move = top - m_ref > kF8RefLimit;
-      const float now = move ? top + kF8RefMargin : m_ref;
+      peak = fmaxf(peak, top);
+      const float at = fmaxf(top, peak - kF8RefFall);
+      const bool fall = at - m_ref < kF8RefFloor && sums < kF8MassFloor * (float)(j + 1) && top > -INFINITY;
+      const bool move = at - m_ref > kF8RefLimit || fall;
+      const float now = move ? at + kF8RefMargin : m_ref;
       const float factor = move ? ex2_approx(m_ref - now) : 1.f;
       // nothing to rescale before the first PV
       const uint32_t moved = j > 0 ? __ballot_sync(0xffffffffu, move) & 0xffffu : 0u;
@@ -780,10 +808,12 @@ sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const uint8_t
       }
       m_ref = now;
       l *= factor;
+      mass *= factor;
 
       // P and its limbs, four positions a word.
       uint32_t p_hi[8], p_lo[8];
       uint64_t l2[2] = {0, 0};
+      __half2 sum2 = __float2half2_rn(0.f);
       const uint64_t minus_m = pack_f32x2(-m_ref, -m_ref);
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
@@ -793,12 +823,14 @@ sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const uint8_t
         l2[0] = fma_f32x2(pack_f32x2(p0, p1), r.x, l2[0]);
         l2[1] = fma_f32x2(pack_f32x2(p2, p3), r.y, l2[1]);
         const uint32_t f01 = pack_f16x2_sat(p0, p1), f23 = pack_f16x2_sat(p2, p3);
+        sum2 = __hadd2(sum2, __hadd2(*reinterpret_cast<const __half2*>(&f01), *reinterpret_cast<const __half2*>(&f23)));
         const uint32_t a01 = limb_first(f01), a23 = limb_first(f23);
         p_hi[q] = limb_bytes_positive(a01, a23);
-        p_lo[q] = limb_bytes(limb_first(half2_bits(limb_rest(f01, a01))), limb_first(half2_bits(limb_rest(f23, a23))));
+        p_lo[q] = limb_bytes_e5m2(limb_rest(f01, a01), limb_rest(f23, a23));
       }
       const float2 l01 = unpack_f32x2(add_f32x2(l2[0], l2[1]));
       l += l01.x + l01.y;
+      mass += __low2float(sum2) + __high2float(sum2);
 
       if (j >= 2) wait_cluster(smem_u32(&bars->p_free[j & 1]), ((j >> 1) - 1) & 1, ab);  // tile j - 2's lo limbs lay where the hi limbs go
       const uint32_t hi_at = s0 + f8_p_at(kPair, j, 0) + rank * kF8Limb, lo_at = s0 + f8_p_at(kPair, j, 1) + rank * kF8Limb;
@@ -813,6 +845,9 @@ sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const uint8_t
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars->p_own[j & 1]));
+      // (for the next tile; the other warp has read the last one's)
+      const float half = mass + __shfl_xor_sync(0xffffffffu, mass, 16);
+      if (hi_row) red[((j & 1) ^ 1) * (2 * kF8Heads) + (4 + ch) * kF8Heads + hd] = half;
 
       // The heads of either CTA that moved: their columns of this CTA's O,
       // between PV(j - 1) and PV(j); 16 columns that hold none of them are left

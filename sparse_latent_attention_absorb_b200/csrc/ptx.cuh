@@ -505,6 +505,9 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, bool a_mn_ma
          | ((uint32_t)(M >> 4) << 24);
 }
 
+// Added to idesc_e4m3_f32: B in E5M2.
+constexpr uint32_t kIdescBE5m2 = 1u << 10;
+
 // Byte offset of 16-byte chunk `chunk` (0..7) of row `row` inside a
 // 128B-swizzled block whose rows are 128 bytes apart.
 __host__ __device__ __forceinline__ uint32_t sw128_offset(uint32_t row, uint32_t chunk) {
