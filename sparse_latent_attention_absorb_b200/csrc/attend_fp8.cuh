@@ -258,6 +258,7 @@ struct F8Bars {
   uint64_t drained[2];    // the MMAs of an aborted kernel
   uint32_t tmem_addr;
   int abort_flag;
+  int selected;           // 0: the split has no valid position
 };
 static_assert(sizeof(F8Bars) <= 512, "barrier block");
 
@@ -316,6 +317,7 @@ sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const uint8_t
     // (the lanes share the barriers: one thread took a microsecond)
     if (lane == 0) {
       bars->abort_flag = 0;
+      bars->selected = 1;
       mbar_init(smem_u32(&bars->q_tma), 1);
       mbar_init(smem_u32(&bars->q_full), kF8SoftmaxWarps);
       mbar_init(smem_u32(&bars->s_full), 1);
@@ -406,6 +408,7 @@ sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const uint8_t
     };
     Four cur = load(0), next = load(1);
     float sv[4], sv_next[4];
+    int selected = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) sv[i] = cur.pos[i] >= 0 ? __ldg(sc_row + (cur.pos[i] >> block_shift)) : 0.f;
     for (int j = 0; j < n_tiles; ++j) {
@@ -419,10 +422,12 @@ sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const uint8_t
         const int n = 32 * i + lane;
         const bool on = !(sv[i] <= 0.f);
         pos_s[(j & 3) * kF8Nt + n] = cur.pos[i];
+        selected |= cur.pos[i] >= 0;
         kt[n] = sv[i];
         kt[kF8Nt + n] = on ? __log2f(sv[i]) : -INFINITY;
         kt[2 * kF8Nt + n] = on ? __frcp_rn(sv[i]) : 0.f;
       }
+      if (j == n_tiles - 1 && !__any_sync(0xffffffffu, selected)) bars->selected = 0;
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars->tile_full[j & 3]));
       prefetch(next);
@@ -905,7 +910,7 @@ sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const uint8_t
         st_async_b32(cluster_map(smem_u32(&fin[h0 + hd]), peer), __float_as_uint(inv), cluster_map(smem_u32(&bars->fin_full), peer));
       if (hd < live)
         lse_part[((size_t)b * n_split + split) * n_heads + h0 + hd] =
-            sum == 0.f ? -INFINITY : (m_ref + log2f(sum)) * 0.6931471805599453f;
+            sum == 0.f || !bars->selected ? -INFINITY : (m_ref + log2f(sum)) * 0.6931471805599453f;
     }
     // the last PV ends after all others
     wait_cluster(smem_u32(&bars->p_free[(n_tiles - 1) & 1]), ((n_tiles - 1) >> 1) & 1, ab);
@@ -930,6 +935,10 @@ sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const uint8_t
     named_bar_sync(1, kSoftmaxThreads);
     if (kPair) wait_cluster(smem_u32(&bars->fin_full), 0, ab);
     const uint32_t lane_base = (uint32_t)(qd * 32) << 16;
+    // (a query that is not finite makes P NaN at masked positions too: beside
+    // valid ones, whose P is NaN then, that changes nothing, and without any it
+    // must not show)
+    const bool none = !bars->selected;
     uint32_t* o_row = reinterpret_cast<uint32_t*>(o_part + ((size_t)b * n_split + split) * n_heads * kDl) + rank * 128 + 16 * qd + (lane >> 1);
     auto write = [&](int cc, const uint32_t (&ov)[32]) {
       const int c0 = 128 * ch + 32 * cc, m = c0 / kCols, hb = c0 % kCols + (lane & 1);
@@ -939,8 +948,8 @@ sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const uint8_t
         const float4 f = f4[i];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const float x = __uint_as_float(ov[4 * i + 2 * u]) * (u ? f.z : f.x);
-          const float y = __uint_as_float(ov[4 * i + 2 * u + 1]) * (u ? f.w : f.y);
+          const float x = none ? 0.f : __uint_as_float(ov[4 * i + 2 * u]) * (u ? f.z : f.x);
+          const float y = none ? 0.f : __uint_as_float(ov[4 * i + 2 * u + 1]) * (u ? f.w : f.y);
           const float other = __shfl_xor_sync(0xffffffffu, (lane & 1) ? x : y, 1);
           const uint32_t w = (lane & 1) ? pack_bf16x2(other, y) : pack_bf16x2(x, other);
           const int head = hb + 4 * i + 2 * u;
