@@ -8,6 +8,7 @@ been built, loading it raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -140,6 +141,24 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _on(stream):
+    """What a call makes for itself is made under the stream that it runs on:
+    memory of the current stream's pool would be free for that stream's work at
+    once, and might still be read by what is queued there."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    return torch.cuda.stream(stream)
+
+
+def _empty(shape, dtype, device, stream):
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _on(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _check(t: torch.Tensor, name: str, dtype, shape=None):
     # one cheap test on the hot path; the detailed checks below only run to
     # name what is wrong
@@ -203,7 +222,7 @@ def mla_sparse_decode(q_nope, q_pe, kv_cache, pe_cache, end_pos, topk_idx, wkv_b
     _check(topk_idx, "topk_idx", torch.int32, (B, K))
     _check(wkv_b, "wkv_b", bf, (H * (D_NOPE + D_V), D_LAT))
     if out is None:
-        out = torch.empty((B, H, D_V), dtype=bf, device=q_nope.device)
+        out = _empty((B, H, D_V), dtype=bf, device=q_nope.device, stream=stream)
     _check(out, "out", bf, (B, H, D_V))
     if lse_out is not None:
         _check(lse_out, "lse_out", torch.float32, (B, H))
@@ -211,7 +230,7 @@ def mla_sparse_decode(q_nope, q_pe, kv_cache, pe_cache, end_pos, topk_idx, wkv_b
         _check(d_status, "d_status", torch.int32, (1,))
     need = workspace_size(B, K, S_max)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q_nope.device)
+        workspace = _empty(need, dtype=torch.uint8, device=q_nope.device, stream=stream)
     _check(workspace, "workspace", torch.uint8)
     rc = lib.mla_sparse_decode(_ptr(q_nope), _ptr(q_pe), _ptr(kv_cache), _ptr(pe_cache), _ptr(end_pos),
                                _ptr(topk_idx), _ptr(wkv_b), float(scale), _ptr(out), B, K, S_max, _ptr(workspace),
@@ -227,7 +246,7 @@ def mla_absorb_q(q_nope, wkv_b, q_lat=None, stream=None):
     _check(q_nope, "q_nope", bf, (B, H, D_NOPE))
     _check(wkv_b, "wkv_b", bf, (H * (D_NOPE + D_V), D_LAT))
     if q_lat is None:
-        q_lat = torch.empty((B, H, D_LAT), dtype=bf, device=q_nope.device)
+        q_lat = _empty((B, H, D_LAT), dtype=bf, device=q_nope.device, stream=stream)
     _check(q_lat, "q_lat", bf, (B, H, D_LAT))
     _raise(lib.mla_absorb_q(_ptr(q_nope), _ptr(wkv_b), _ptr(q_lat), B, _stream(stream)), "mla_absorb_q")
     return q_lat
@@ -259,9 +278,9 @@ def mla_sparse_attend(q_lat, q_pe, kv_cache, pe_cache, end_pos, topk_idx, scale,
     dev = q_lat.device
     o_shape, o_dtype = _o_part_spec(B, n_split)
     if o_part is None:
-        o_part = torch.empty(o_shape, dtype=o_dtype, device=dev)
+        o_part = _empty(o_shape, dtype=o_dtype, device=dev, stream=stream)
     if lse_part is None:
-        lse_part = torch.empty((B, n_split, H), dtype=torch.float32, device=dev)
+        lse_part = _empty((B, n_split, H), dtype=torch.float32, device=dev, stream=stream)
     _check(o_part, "o_part", o_dtype, o_shape)
     _check(lse_part, "lse_part", torch.float32, (B, n_split, H))
     rc = lib.mla_sparse_attend(_ptr(q_lat), _ptr(q_pe), _ptr(kv_cache), _ptr(pe_cache), _ptr(end_pos),
@@ -281,7 +300,7 @@ def mla_combine_value_up(o_part, lse_part, wkv_b, out=None, lse_out=None, stream
     _check(lse_part, "lse_part", torch.float32, (B, n_split, H))
     _check(wkv_b, "wkv_b", bf, (H * (D_NOPE + D_V), D_LAT))
     if out is None:
-        out = torch.empty((B, H, D_V), dtype=bf, device=o_part.device)
+        out = _empty((B, H, D_V), dtype=bf, device=o_part.device, stream=stream)
     _check(out, "out", bf, (B, H, D_V))
     if lse_out is not None:
         _check(lse_out, "lse_out", torch.float32, (B, H))
@@ -353,7 +372,7 @@ def mla_output_projection(x, wo, delta=None, workspace=None, d_status=None, stre
     _check(x, "x", bf)
     _check(wo, "wo", bf, (dim, H * D_V))
     if delta is None:
-        delta = torch.empty((B, dim), dtype=bf, device=x.device)
+        delta = _empty((B, dim), dtype=bf, device=x.device, stream=stream)
     _check(delta, "delta", bf, (B, dim))
     if d_status is not None:
         _check(d_status, "d_status", torch.int32, (1,))
@@ -361,7 +380,7 @@ def mla_output_projection(x, wo, delta=None, workspace=None, d_status=None, stre
         need = projection_workspace_size(B, dim)
         if need == 0:
             raise MLAError(1, "mla_output_projection")
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = _empty(need, dtype=torch.uint8, device=x.device, stream=stream)
     _check(workspace, "workspace", torch.uint8)
     rc = lib.mla_output_projection(_ptr(x), _ptr(wo), _ptr(delta), B, dim, _ptr(workspace), workspace.numel(),
                                    _ptr(d_status), _stream(stream))
@@ -395,7 +414,7 @@ def mla_sparse_decode_project(q_nope, q_pe, kv_cache, pe_cache, end_pos, topk_id
     _check(wkv_b, "wkv_b", bf, (H * (D_NOPE + D_V), D_LAT))
     _check(wo, "wo", bf, (dim, H * D_V))
     if delta is None:
-        delta = torch.empty((B, dim), dtype=bf, device=q_nope.device)
+        delta = _empty((B, dim), dtype=bf, device=q_nope.device, stream=stream)
     _check(delta, "delta", bf, (B, dim))
     if lse_out is not None:
         _check(lse_out, "lse_out", torch.float32, (B, H))
@@ -405,7 +424,7 @@ def mla_sparse_decode_project(q_nope, q_pe, kv_cache, pe_cache, end_pos, topk_id
         need = project_workspace_size(B, K, S_max, dim)
         if need == 0:
             raise MLAError(1, "mla_sparse_decode_project")
-        workspace = torch.empty(need, dtype=torch.uint8, device=q_nope.device)
+        workspace = _empty(need, dtype=torch.uint8, device=q_nope.device, stream=stream)
     _check(workspace, "workspace", torch.uint8)
     rc = lib.mla_sparse_decode_project(_ptr(q_nope), _ptr(q_pe), _ptr(kv_cache), _ptr(pe_cache), _ptr(end_pos),
                                        _ptr(topk_idx), _ptr(wkv_b), float(scale), _ptr(wo), _ptr(delta), B, K,
@@ -433,14 +452,14 @@ def mla_sparse_prefill(q_nope, q_pe, kv_cache, pe_cache, cache_slot, end_pos, to
     _check(topk_idx, "topk_idx", torch.int32, (R, K))
     _check(wkv_b, "wkv_b", bf, (H * (D_NOPE + D_V), D_LAT))
     if out is None:
-        out = torch.empty((R, H, D_V), dtype=bf, device=q_nope.device)
+        out = _empty((R, H, D_V), dtype=bf, device=q_nope.device, stream=stream)
     _check(out, "out", bf, (R, H, D_V))
     if lse_out is not None:
         _check(lse_out, "lse_out", torch.float32, (R, H))
     if d_status is not None:
         _check(d_status, "d_status", torch.int32, (1,))
     if workspace is None:
-        workspace = torch.empty(workspace_size(R, K, S_max), dtype=torch.uint8, device=q_nope.device)
+        workspace = _empty(workspace_size(R, K, S_max), dtype=torch.uint8, device=q_nope.device, stream=stream)
     _check(workspace, "workspace", torch.uint8)
     rc = lib.mla_sparse_prefill(_ptr(q_nope), _ptr(q_pe), _ptr(kv_cache), _ptr(pe_cache), _ptr(cache_slot),
                                 _ptr(end_pos), _ptr(topk_idx), _ptr(wkv_b), float(scale), _ptr(out), R, K, S_max,
@@ -455,8 +474,9 @@ def selftest_wait_timeout(stream=None):
     result bits) as the library wrote them: (MLA_ERR_DEVICE_TIMEOUT, 4) when
     healthy."""
     lib = load_library()
-    status = torch.zeros(1, dtype=torch.int32, device="cuda")
-    result = torch.full((1,), -1, dtype=torch.int32, device="cuda")
+    with _on(stream):
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        result = torch.full((1,), -1, dtype=torch.int32, device="cuda")
     _raise(lib.mla_selftest_wait_timeout(_ptr(status), _ptr(result), _stream(stream)), "mla_selftest_wait_timeout")
     torch.cuda.synchronize()
     return int(status.item()), int(result.item())
@@ -472,7 +492,7 @@ def mla_check_topk_indices(end_pos, topk_idx, S_max: int, d_status=None, row_fla
     _check(end_pos, "end_pos", torch.int32, (B,))
     _check(topk_idx, "topk_idx", torch.int32)
     if d_status is None and row_flags is None:
-        row_flags = torch.empty(B, dtype=torch.int32, device=topk_idx.device)
+        row_flags = _empty(B, dtype=torch.int32, device=topk_idx.device, stream=stream)
     if row_flags is not None:
         _check(row_flags, "row_flags", torch.int32, (B,))
     if d_status is not None:
@@ -507,7 +527,7 @@ def mla_sparse_decode_heads(q_nope, q_pe, kv_cache, pe_cache, end_pos, topk_idx,
     _check(topk_idx, "topk_idx", torch.int32, (B, K))
     _check(wkv_b, "wkv_b", bf, (n_heads * (D_NOPE + D_V), D_LAT))
     if out is None:
-        out = torch.empty((B, n_heads, D_V), dtype=bf, device=q_nope.device)
+        out = _empty((B, n_heads, D_V), dtype=bf, device=q_nope.device, stream=stream)
     _check(out, "out", bf, (B, n_heads, D_V))
     if lse_out is not None:
         _check(lse_out, "lse_out", torch.float32, (B, n_heads))
@@ -515,7 +535,7 @@ def mla_sparse_decode_heads(q_nope, q_pe, kv_cache, pe_cache, end_pos, topk_idx,
         n = lib.mla_sparse_decode_heads_workspace_size(B, K, S_max, n_heads)
         if n == 0:
             raise MLAError(1, "mla_sparse_decode_heads_workspace_size")
-        workspace = torch.empty(n, dtype=torch.uint8, device=q_nope.device)
+        workspace = _empty(n, dtype=torch.uint8, device=q_nope.device, stream=stream)
     _check(workspace, "workspace", torch.uint8)
     rc = lib.mla_sparse_decode_heads(_ptr(q_nope), _ptr(q_pe), _ptr(kv_cache), _ptr(pe_cache), _ptr(end_pos),
                                      _ptr(topk_idx), _ptr(wkv_b), float(scale), _ptr(out), B, K, S_max, n_heads,
@@ -537,13 +557,13 @@ def mla_output_projection_shard(x, wo, delta=None, workspace=None, d_status=None
     if not (wo.is_cuda and wo.dtype == torch.bfloat16 and wo.dim() == 2 and wo.shape[1] == k_in and wo.stride(1) == 1):
         raise ValueError("wo: expected a CUDA bf16 [dim, k_in] view with unit column stride")
     if delta is None:
-        delta = torch.empty((B, dim), dtype=torch.bfloat16, device=x.device)
+        delta = _empty((B, dim), dtype=torch.bfloat16, device=x.device, stream=stream)
     _check(delta, "delta", torch.bfloat16, (B, dim))
     if workspace is None:
         n = lib.mla_output_projection_shard_workspace_size(B, dim, k_in)
         if n == 0:
             raise MLAError(1, "mla_output_projection_shard_workspace_size")
-        workspace = torch.empty(n, dtype=torch.uint8, device=x.device)
+        workspace = _empty(n, dtype=torch.uint8, device=x.device, stream=stream)
     _check(workspace, "workspace", torch.uint8)
     rc = lib.mla_output_projection_shard(_ptr(x), _ptr(wo), wo.stride(0), _ptr(delta), B, dim, k_in, _ptr(workspace),
                                          workspace.numel(), _ptr(d_status), _stream(stream))
@@ -567,7 +587,7 @@ def mla_prepare_wo(wo, stream=None) -> PreparedWo:
     if not (wo.is_cuda and wo.dtype == torch.bfloat16 and wo.dim() == 2 and wo.stride(1) == 1):
         raise ValueError("wo: expected a CUDA bf16 [dim, k_in] view with unit column stride")
     dim, k_in = wo.shape
-    data = torch.empty(dim * k_in, dtype=torch.bfloat16, device=wo.device)
+    data = _empty(dim * k_in, dtype=torch.bfloat16, device=wo.device, stream=stream)
     _raise(lib.mla_prepare_wo(_ptr(wo), wo.stride(0), dim, k_in, _ptr(data), _stream(stream)), "mla_prepare_wo")
     return PreparedWo(data, dim, k_in)
 
@@ -580,13 +600,13 @@ def mla_output_projection_prepared(x, wo_p: PreparedWo, delta=None, workspace=No
     dim = wo_p.dim
     _check(x, "x", torch.bfloat16, (B, wo_p.k_in))
     if delta is None:
-        delta = torch.empty((B, dim), dtype=torch.bfloat16, device=x.device)
+        delta = _empty((B, dim), dtype=torch.bfloat16, device=x.device, stream=stream)
     _check(delta, "delta", torch.bfloat16, (B, dim))
     if workspace is None:
         n = lib.mla_output_projection_shard_workspace_size(B, dim, k_in)
         if n == 0:
             raise MLAError(1, "mla_output_projection_shard_workspace_size")
-        workspace = torch.empty(n, dtype=torch.uint8, device=x.device)
+        workspace = _empty(n, dtype=torch.uint8, device=x.device, stream=stream)
     _check(workspace, "workspace", torch.uint8)
     rc = lib.mla_output_projection_prepared(_ptr(x), _ptr(wo_p.data), _ptr(delta), B, dim, k_in, _ptr(workspace),
                                             workspace.numel(), _ptr(d_status), _stream(stream))
@@ -605,7 +625,7 @@ def mla_dequant_fp8_blocks(w_fp8, scale, out=None, stream=None):
     _check(w_fp8, "w_fp8", torch.uint8, (rows, cols))
     _check(scale, "scale", torch.float32, ((rows + 127) // 128, (cols + 127) // 128))
     if out is None:
-        out = torch.empty((rows, cols), dtype=torch.bfloat16, device=w_fp8.device)
+        out = _empty((rows, cols), dtype=torch.bfloat16, device=w_fp8.device, stream=stream)
     _check(out, "out", torch.bfloat16, (rows, cols))
     _raise(lib.mla_dequant_fp8_blocks(_ptr(w_fp8), _ptr(scale), _ptr(out), rows, cols, _stream(stream)),
            "mla_dequant_fp8_blocks")
@@ -698,7 +718,7 @@ def mla_sparse_decode_fp8(q_nope, q_pe, cache: Fp8Cache, end_pos, topk_idx, wkv_
     if cache_slot is not None:
         _check(cache_slot, "cache_slot", torch.int32, (R,))
     if out is None:
-        out = torch.empty((R, n_heads, D_V), dtype=bf, device=q_nope.device)
+        out = _empty((R, n_heads, D_V), dtype=bf, device=q_nope.device, stream=stream)
     _check(out, "out", bf, (R, n_heads, D_V))
     if lse_out is not None:
         _check(lse_out, "lse_out", torch.float32, (R, n_heads))
@@ -708,7 +728,7 @@ def mla_sparse_decode_fp8(q_nope, q_pe, cache: Fp8Cache, end_pos, topk_idx, wkv_
         need = workspace_size_fp8(R, K, S_max, n_heads)
         if need == 0:
             raise MLAError(1, "mla_sparse_decode_fp8")
-        workspace = torch.empty(need, dtype=torch.uint8, device=q_nope.device)
+        workspace = _empty(need, dtype=torch.uint8, device=q_nope.device, stream=stream)
     _check(workspace, "workspace", torch.uint8)
     _check_same_device(q_nope.device, q_pe=q_pe, cache=cache.kv, end_pos=end_pos, topk_idx=topk_idx, wkv_b=wkv_b,
                        cache_slot=cache_slot, out=out, workspace=workspace, lse_out=lse_out, d_status=d_status)
@@ -735,9 +755,9 @@ def mla_sparse_attend_fp8(q_lat, q_pe, cache: Fp8Cache, end_pos, topk_idx, scale
     if cache_slot is not None:
         _check(cache_slot, "cache_slot", torch.int32, (R,))
     if o_part is None:
-        o_part = torch.empty((R, n_split, n_heads, D_LAT), dtype=bf, device=q_lat.device)
+        o_part = _empty((R, n_split, n_heads, D_LAT), dtype=bf, device=q_lat.device, stream=stream)
     if lse_part is None:
-        lse_part = torch.empty((R, n_split, n_heads), dtype=torch.float32, device=q_lat.device)
+        lse_part = _empty((R, n_split, n_heads), dtype=torch.float32, device=q_lat.device, stream=stream)
     _check(o_part, "o_part", bf, (R, n_split, n_heads, D_LAT))
     _check(lse_part, "lse_part", torch.float32, (R, n_split, n_heads))
     if d_status is not None:
@@ -822,7 +842,7 @@ def mla_accumulate_weights_fp8(q_lat, q_pe, cache: Fp8Cache, end_pos, topk_idx, 
     return acc
 
 
-def _evict_outputs(acc, end_pos, keep, recent, acc_out, kept, new_end, in_place, **tensors):
+def _evict_outputs(acc, end_pos, keep, recent, acc_out, kept, new_end, in_place, stream, **tensors):
     """Checks what both evictions share; returns (B, S_max, acc_out, kept, new_end)."""
     if not isinstance(acc, torch.Tensor) or acc.dim() != 2:
         raise ValueError("acc: expected a tensor [B, S_max]")
@@ -838,9 +858,9 @@ def _evict_outputs(acc, end_pos, keep, recent, acc_out, kept, new_end, in_place,
         acc_out = acc
     _check(acc_out, "acc_out", torch.float32, (B, S_max))
     if kept is None:
-        kept = torch.empty((B, keep), dtype=torch.int32, device=acc.device)
+        kept = _empty((B, keep), dtype=torch.int32, device=acc.device, stream=stream)
     if new_end is None:
-        new_end = torch.empty(B, dtype=torch.int32, device=acc.device)
+        new_end = _empty(B, dtype=torch.int32, device=acc.device, stream=stream)
     _check(kept, "kept", torch.int32, (B, keep))
     _check(new_end, "new_end", torch.int32, (B,))
     _check_same_device(acc.device, end_pos=end_pos, acc_out=acc_out, kept=kept, new_end=new_end, **tensors)
@@ -858,7 +878,7 @@ def mla_evict(kv_cache, pe_cache, acc, end_pos, keep: int, recent: int, kv_out=N
     if (pe_out is None) != in_place or (acc_out is None) != in_place:
         raise ValueError("kv_out, pe_out and acc_out: give all of them, or none (in place)")
     B, S_max, acc_out, kept, new_end = _evict_outputs(acc, end_pos, keep, recent, acc_out, kept, new_end, in_place,
-                                                      kv_cache=kv_cache, pe_cache=pe_cache, kv_out=kv_out,
+                                                      stream, kv_cache=kv_cache, pe_cache=pe_cache, kv_out=kv_out,
                                                       pe_out=pe_out)
     kv_out, pe_out = (kv_cache, pe_cache) if in_place else (kv_out, pe_out)
     for name, t, d in (("kv_cache", kv_cache, D_LAT), ("pe_cache", pe_cache, D_ROPE), ("kv_out", kv_out, D_LAT),
@@ -880,7 +900,7 @@ def mla_evict_fp8(cache: Fp8Cache, acc, end_pos, keep: int, recent: int, cache_o
         raise ValueError("cache_out and acc_out: give both, or neither (in place)")
     to = cache if in_place else cache_out
     B, S_max, acc_out, kept, new_end = _evict_outputs(acc, end_pos, keep, recent, acc_out, kept, new_end, in_place,
-                                                      cache=cache.kv, cache_out=to.kv)
+                                                      stream, cache=cache.kv, cache_out=to.kv)
     if (cache.S_max, to.S_max) != (S_max, S_max) or cache.block != to.block or min(cache.n_slots, to.n_slots) < B:
         raise ValueError(f"cache, cache_out: expected at least {B} slots of {S_max} positions and one block size")
     rc = lib.mla_evict_fp8(_ptr(cache.kv), _ptr(cache.pe), _ptr(cache.scale), cache.block, _ptr(acc), _ptr(end_pos),
