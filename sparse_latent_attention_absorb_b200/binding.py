@@ -662,6 +662,9 @@ class Fp8Cache:
         _check(kv, "kv", torch.uint8, (n_slots, S_max, D_LAT))
         _check(pe, "pe", torch.bfloat16, (n_slots, S_max, D_ROPE))
         _check(scale, "scale", torch.float32, (n_slots, (S_max + block - 1) // block))
+        for name, t in (("pe", pe), ("scale", scale)):  # (the calls look at kv alone)
+            if t.get_device() != kv.get_device():
+                raise ValueError(f"{name}: on {t.device}, expected {kv.device}")
         self.kv, self.pe, self.scale, self.block = kv, pe, scale, block
         self.n_slots, self.S_max = n_slots, S_max
 
@@ -796,7 +799,7 @@ def mla_append_fp8(cache: Fp8Cache, kv_new, pe_new, cu_rows, start_pos, cache_sl
     return cache
 
 
-def _check_weights(q_lat, q_pe, end_pos, topk_idx, lse, acc, S_max, cache, d_status):
+def _check_weights(q_lat, q_pe, end_pos, topk_idx, lse, acc, S_max, d_status, **cache):
     B, n_heads = q_lat.shape[0], q_lat.shape[1]
     _check(q_lat, "q_lat", torch.bfloat16, (B, n_heads, D_LAT))
     _check(q_pe, "q_pe", torch.bfloat16, (B, n_heads, D_ROPE))
@@ -806,8 +809,8 @@ def _check_weights(q_lat, q_pe, end_pos, topk_idx, lse, acc, S_max, cache, d_sta
     _check(acc, "acc", torch.float32, (B, S_max))
     if d_status is not None:
         _check(d_status, "d_status", torch.int32, (1,))
-    _check_same_device(q_lat.device, q_pe=q_pe, end_pos=end_pos, topk_idx=topk_idx, lse=lse, acc=acc, cache=cache,
-                       d_status=d_status)
+    _check_same_device(q_lat.device, q_pe=q_pe, end_pos=end_pos, topk_idx=topk_idx, lse=lse, acc=acc,
+                       d_status=d_status, **cache)
     return B, topk_idx.shape[1], n_heads
 
 
@@ -818,7 +821,8 @@ def mla_accumulate_weights(q_lat, q_pe, kv_cache, pe_cache, end_pos, topk_idx, s
     decode step's lse_out.  Returns acc."""
     lib = load_library()
     S_max = kv_cache.shape[1]
-    B, K, n_heads = _check_weights(q_lat, q_pe, end_pos, topk_idx, lse, acc, S_max, kv_cache, d_status)
+    B, K, n_heads = _check_weights(q_lat, q_pe, end_pos, topk_idx, lse, acc, S_max, d_status, kv_cache=kv_cache,
+                                   pe_cache=pe_cache)
     _check(kv_cache, "kv_cache", torch.bfloat16, (B, S_max, D_LAT))
     _check(pe_cache, "pe_cache", torch.bfloat16, (B, S_max, D_ROPE))
     rc = lib.mla_accumulate_weights(_ptr(q_lat), _ptr(q_pe), _ptr(kv_cache), _ptr(pe_cache), _ptr(end_pos),
@@ -832,7 +836,7 @@ def mla_accumulate_weights_fp8(q_lat, q_pe, cache: Fp8Cache, end_pos, topk_idx, 
                                stream=None):
     """mla_accumulate_weights over an 8-bit cache (row b reads slot b)."""
     lib = load_library()
-    B, K, n_heads = _check_weights(q_lat, q_pe, end_pos, topk_idx, lse, acc, cache.S_max, cache.kv, d_status)
+    B, K, n_heads = _check_weights(q_lat, q_pe, end_pos, topk_idx, lse, acc, cache.S_max, d_status, cache=cache.kv)
     if cache.n_slots < B:
         raise ValueError(f"cache: {cache.n_slots} slots for {B} rows")
     rc = lib.mla_accumulate_weights_fp8(_ptr(q_lat), _ptr(q_pe), _ptr(cache.kv), _ptr(cache.pe), _ptr(cache.scale),
