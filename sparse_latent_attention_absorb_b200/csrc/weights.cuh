@@ -347,7 +347,7 @@ accumulate_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __nv_b
     for (int j = 0; j < n_tiles; ++j) {
       float* rt = red + (j & 1) * (4 * kWtNt) + qd * kWtNt + 64 * ch;
       const ulonglong2* kt = reinterpret_cast<const ulonglong2*>(sc + (j & 3) * kWtNt + 64 * ch);
-      const bool known = wait(smem_u32(&bars->tile_full[j & 3]), (j >> 2) & 1, ab);  // else timed out: nothing is added
+      wait(smem_u32(&bars->tile_full[j & 3]), (j >> 2) & 1, ab);
       wait(smem_u32(&bars->s_full[j & 1]), (j >> 1) & 1, ab);
       tc_fence_after();
 #pragma unroll 1
@@ -380,8 +380,10 @@ accumulate_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __nv_b
       if (warp < 4) {
         const float* s4 = red + (j & 1) * (4 * kWtNt) + tid;
         const int pos = pos_s[(j & 3) * kWtNt + tid];
-        // distinct positions: an addition a position, in whatever order
-        if (known && pos >= 0) atomicAdd(acc + (size_t)b * S_max + pos, (s4[0] + s4[kWtNt]) + (s4[2 * kWtNt] + s4[3 * kWtNt]));
+        // Distinct positions: an addition a position, in whatever order.  Once a
+        // wait of any warp has timed out (seen through the barriers since), the
+        // scores may be anything, and nothing is added any more.
+        if (!*ab.flag && pos >= 0) atomicAdd(acc + (size_t)b * S_max + pos, (s4[0] + s4[kWtNt]) + (s4[2 * kWtNt] + s4[3 * kWtNt]));
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars->tile_done[j & 3]));
       }
