@@ -183,9 +183,11 @@ int mla_check_topk_indices(const int32_t* end_pos, const int32_t* topk_idx, int 
 /*
  * Opt-in debug mode for the whole process: with enable != 0, every call of
  * mla_sparse_decode, mla_sparse_prefill and the entry points built on them
- * (noalloc, host-buffer, decode + projection) that is given a d_status
- * first enqueues mla_check_topk_indices on its index rows, so a repeated
- * index ends up as MLA_ERR_BAD_INDEX in *d_status (the decode still runs).
+ * (noalloc, host-buffer, decode + projection, head shards), of
+ * mla_sparse_decode_fp8 and of mla_accumulate_weights(_fp8) that is given a
+ * d_status first enqueues mla_check_topk_indices on its index rows, so a
+ * repeated index ends up as MLA_ERR_BAD_INDEX in *d_status (the call still
+ * runs).
  * Off by default; costs one extra kernel per call.  Returns the previous
  * setting.
  */

@@ -554,7 +554,7 @@ extern "C" int mla_combine_value_up(const void* o_part, const float* lse_part, c
 }
 
 namespace {
-// Opt-in index validation before every decode / prefill call (see
+// Opt-in index validation before every decode, prefill and totals call (see
 // mla_set_index_checks); off by default.
 std::atomic<int> g_index_checks{0};
 
@@ -783,6 +783,9 @@ int run_weights(const void* q_lat, const void* q_pe, const void* kv, const void*
   DeviceInfo* info = nullptr;
   int rc = prepare(&info);
   if (rc != MLA_OK) return rc;
+  if (d_status && g_index_checks.load(std::memory_order_relaxed) &&
+      (rc = launch_check_indices(end_pos, topk_idx, B, K, S_max, d_status, nullptr, stream)) != MLA_OK)
+    return rc;
   // whole 128-slot tiles, as many splits as fill the SMs
   const int tiles = ceil_div(K, kWtNt);
   const int want = B >= info->sm_count ? 1 : (info->sm_count / B < tiles ? info->sm_count / B : tiles);
