@@ -371,6 +371,10 @@ accumulate_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __nv_b
           p[4 * q + 2] = ex2_approx(d.x);
           p[4 * q + 3] = ex2_approx(d.y);
         }
+        if (n_heads < kH) {  // absent heads: zeros, which an infinite row turns into NaN
+#pragma unroll
+          for (int i = 0; i < 32; ++i) p[i] = live ? p[i] : 0.f;
+        }
         rt[32 * r + lane] = sum_transposed(p, lane);
       }
       tc_fence_before();
