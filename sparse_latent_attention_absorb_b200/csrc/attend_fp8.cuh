@@ -107,8 +107,8 @@ __device__ __forceinline__ float rotary_top(const uint4 (&r)[4]) {
   return m < 0x7f80u ? __uint_as_float(m << 16) : 0.f;
 }
 // The common exponent of queries up to `amax` and rotary ones up to `rmax`, which
-// go along as 2^e q_pe: these stay below 2^60, so that no sum of theirs overflows
-// where the others are far smaller.
+// go along as 2^e q_pe: these stay below 2^60 (2^63 in the lo rows), so that no
+// sum of theirs overflows where the others are far smaller.
 __device__ __forceinline__ int query_exponent(float amax, float rmax) {
   const int e = limb_exponent(amax);
   if (!(rmax > 0.f)) return e;
@@ -125,7 +125,7 @@ __device__ __forceinline__ int query_exponent(float amax, float rmax) {
 //                                 queries (TMEM; 16 heads' hi rows, then their
 //                                 lo rows, in every 32 lanes), N = 128 positions
 //                                 (K-major, as gathered), plus the bf16 rotary
-//                                 product into the hi rows.  S_hi + S_lo / 16
+//                                 product, half of it in each.  S_hi + S_lo / 16
 //                                 meets in one shuffle across half a warp;
 //   y[h, t]      = scale s_t S + log2 s_t, the log2 weight of position t's codes;
 //   P[h, t]      = 2^(y - m_h), row sum += P / s_t;
@@ -189,7 +189,7 @@ constexpr int kF8Limb = kF8Nt * kF8Heads;
 __host__ __device__ constexpr int f8_p_at(bool pair, int j, int lo) {
   return f8_own_at(pair, f8_stages(pair), 0) + (pair ? (2 * j + lo) % 3 * (2 * kF8Limb) : (j & 1) * (2 * kF8Limb) + lo * kF8Limb);
 }
-constexpr int kF8OffQpe = 12 * kF8Block;                     // 128 rows (the lo rows are zero)
+constexpr int kF8OffQpe = 12 * kF8Block;                     // 128 rows
 constexpr int kF8OffKey = kF8OffQpe + kF8Block;              // f32 [4][3][128]: what a position's scale enters by
 constexpr int kF8OffPos = kF8OffKey + 4 * 3 * kF8Nt * 4;     // int [4][128]: a tile's positions, -1 = masked
 constexpr int kF8OffRed = kF8OffPos + 4 * kF8Nt * 4;         // f32 [4][2][64]
@@ -632,7 +632,7 @@ sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const uint8_t
       uint4 r4[4];
       const uint4* psrc = reinterpret_cast<const uint4*>(q_pe + ((size_t)b * n_heads + h0 + hd) * kDr) + 4 * ch;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) r4[u] = hi_row && hd < live ? __ldg(psrc + u) : make_uint4(0, 0, 0, 0);
+      for (int u = 0; u < 4; ++u) r4[u] = hd < live ? __ldg(psrc + u) : make_uint4(0, 0, 0, 0);
 
       // scaled (fp16): the exponents of the thread's two times 128 columns
       const bool scaled = q_exp != nullptr;
@@ -676,13 +676,16 @@ sparse_attend_fp8_kernel(const __grid_constant__ CUtensorMap tm_q, const uint8_t
       const int e = query_exponent(am, rm);
       const float mul = exp2_int(e);
       c2 = scale * 1.4426950408889634f * exp2_int(-e);
+      // The rotary factors in both rows of a head, half in each (S_lo counts a
+      // 16th): a zero would turn a key's infinity into NaN.
+      const float mul_r = hi_row ? 0.5f * mul : (0.5f / kLimbLo) * mul;
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const uint32_t w[4] = {r4[u].x, r4[u].y, r4[u].z, r4[u].w};
         uint32_t o[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)  // times a power of two: exact
-          o[i] = pack_bf16x2(__uint_as_float(w[i] << 16) * mul, __uint_as_float(w[i] & 0xffff0000u) * mul);
+          o[i] = pack_bf16x2(__uint_as_float(w[i] << 16) * mul_r, __uint_as_float(w[i] & 0xffff0000u) * mul_r);
         st_shared_v4(s0 + kF8OffQpe + sw128_offset(32 * qd + lane, 4 * ch + u), o[0], o[1], o[2], o[3]);
       }
       fence_proxy_async_smem();
