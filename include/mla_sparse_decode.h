@@ -458,13 +458,16 @@ int mla_output_projection_prepared(const void* x, const void* wo_prepared, void*
  *   workspace  mla_sparse_decode_fp8_workspace_size(R, K, S_max, n_heads)
  * The latent queries enter the scores with nine significant bits and the
  * rotary ones as given, the codes exactly; scores and row sums are f32.  The
- * softmax weights enter the mix with eight significant bits, as bf16 weights
+ * queries of 64 heads (0 to 63, 64 to 127) share one power of two: what is 2^-18
+ * of the largest of them (or 2^-70 of the largest rotary factor) is lost, and
+ * scores are that exact.  (The step forms them in fp16 in units of the bound 128
+ * max|q_nope| max|W_UK| of a row, a head and 128 latent columns: where they all
+ * lie 2^22 below that bound, they have bf16's digits, and fewer further down.)
+ * The softmax weights enter the mix with eight significant bits, as bf16 weights
  * would, where weight times scale is at least 2^-7 of the largest of the same
  * 128 index slots; what is smaller is off by at most 2^-15 of that one or, if it
  * is more, of the mean of the sums of the 128-slot tiles so far (a tile's 128
- * together by 2^-8 of it).  The queries of 64 heads (0 to 63, 64 to 127) share one power of two:
- * what is 2^-18 of the largest of them (or 2^-70 of the largest rotary factor)
- * is lost, and scores are that exact.
+ * together by 2^-8 of it).
  *
  * mla_sparse_attend_fp8: steps "scores" .. "mix" alone, as mla_sparse_attend
  * (o_part bf16 [R,n_split,n_heads,512], lse_part f32 [R,n_split,n_heads];
@@ -501,9 +504,11 @@ int mla_sparse_attend_fp8(const void* q_lat, const void* q_pe, const void* kv_fp
  * its rows (at least 2^-40); codes are kv / s rounded to E4M3 (nearest, ties to
  * even), pe becomes pe_new / s in bf16.  Positions of a block before a
  * sequence's first row are taken to hold rows: s is then at least their scale,
- * and where it has to grow they are rounded again to it.  Positions behind the
- * last row are not touched.  Infinite and NaN latents become NaN and do not
- * count for s.  16-byte aligned pointers.  Two sequences of a call, or two
+ * and where it has to grow they are rounded again to it.  Positions of a block
+ * behind a sequence's last row are taken to be dead: their codes stay, but the
+ * scale that they share is the new rows', larger or smaller, and they stand for
+ * other numbers then.  Infinite and NaN latents become NaN and do not count for
+ * s.  1 <= N <= 2^24; 16-byte aligned pointers.  Two sequences of a call, or two
  * calls that overlap on the GPU, may not write the same block.  Returns an
  * mla_status.
  */
@@ -515,9 +520,11 @@ int mla_append_fp8(const void* kv_new, const void* pe_new, const int32_t* cu_row
  * The attention weights of a decode step, summed over the heads and added to
  * running totals (no counterpart on the pages: mla_evict goes by them):
  *   acc[b,t] += sum_h exp(score[b,h,t] - lse[b,h])   for the selected t of row b
- *   q_lat bf16 [B,n_heads,512] (mla_absorb_q), q_pe bf16 [B,n_heads,64], the
- *         caches, end_pos, topk_idx, scale: as the decode step was given them
- *         (row b reads slot b); n_heads 1 to 128
+ *   q_lat bf16 [B,n_heads,512] (mla_absorb_q makes it for all 128 heads; for a
+ *         head shard it is the caller's product of q_nope and W_UK), q_pe bf16
+ *         [B,n_heads,64], the caches, end_pos, topk_idx, scale: as the decode
+ *         step was given them.  Row b reads slot b (there is no cache_slot);
+ *         n_heads 1 to 128
  *   lse   f32 [B,n_heads], the decode step's lse_out
  *   acc   f32 [B,S_max], read and written at the selected positions only
  * A position's total gets one addition a call (valid indices are distinct), so

@@ -817,8 +817,10 @@ def _check_weights(q_lat, q_pe, end_pos, topk_idx, lse, acc, S_max, d_status, **
 def mla_accumulate_weights(q_lat, q_pe, kv_cache, pe_cache, end_pos, topk_idx, scale, lse, acc, d_status=None,
                            stream=None):
     """Adds the attention weight of every selected position, summed over the
-    heads, to acc (f32 [B, S_max], in place); q_lat from mla_absorb_q, lse the
-    decode step's lse_out.  Returns acc."""
+    heads, to acc (f32 [B, S_max], in place); q_lat (bf16 [B, n_heads, 512])
+    from mla_absorb_q, which makes it for all 128 heads, or from the caller's
+    own product for a head shard; lse the decode step's lse_out.  Row b reads
+    slot b.  Returns acc."""
     lib = load_library()
     S_max = kv_cache.shape[1]
     B, K, n_heads = _check_weights(q_lat, q_pe, end_pos, topk_idx, lse, acc, S_max, d_status, kv_cache=kv_cache,

@@ -20,7 +20,7 @@ LIB_NAME = "libmla_sparse_decode.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 SOURCES = [os.path.join(CSRC, "mla_sparse_decode.cu"), os.path.join(CSRC, "selftest.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in ("kernels.cuh", "ptx.cuh", "projection.cuh", "projection_plan.h", "index_check.cuh", "dequant.cuh", "attend_fp8.cuh",
-                                                          "append_fp8.cuh", "weights.cuh", "evict.cuh")] + [
+                                                          "append_fp8.cuh", "append_plan.h", "weights.cuh", "evict.cuh")] + [
     os.path.join(INCLUDE, "mla_sparse_decode.h")]
 
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]

@@ -19,6 +19,7 @@
 #include <cuda_fp8.h>
 #include <cstdint>
 
+#include "append_plan.h"
 #include "attend_fp8.cuh"
 
 namespace mla {
@@ -155,11 +156,7 @@ append_fp8_rows_kernel(const AppendArgs a) {
 // kHold rows of a warp held in registers between the maximum and the rounding
 // (the others are read twice, the second time from L1 or L2): two where a block
 // has no more (16 positions), and six CTAs an SM then, else four.
-//
-// Sequence q's blocks are the CTAs from cu[q] / block + 2 q on: L tokens touch
-// at most L / block + 2 blocks, so they end before the next sequence's, and the
-// CTAs behind them return.
-__host__ __device__ inline int append_blocks_grid(int N, int n_seq, int shift) { return (N >> shift) + 2 * n_seq; }
+// (Which block a CTA takes: append_plan.h.)
 
 template <int kHold>
 __global__ void __launch_bounds__(kAppendThreads, kHold == 2 ? 6 : 4)
@@ -167,19 +164,15 @@ append_fp8_blocks_kernel(const AppendArgs a) {
   constexpr int kWarps = kAppendThreads / 32;
   __shared__ float tops[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, at = (int)blockIdx.x;
-  auto first_cta = [&](int q) { return (min(max(__ldg(a.cu_rows + q), 0), a.N) >> a.shift) + 2 * q; };
+  auto first_cta = [&](int q) { return append_first_cta(__ldg(a.cu_rows + q), a.N, q, a.shift); };
   const int seq = count_at_most(first_cta, a.n_seq, at, lane);
   if (seq >= a.n_seq) return;
   const int row0 = __ldg(a.cu_rows + seq), row1 = min(__ldg(a.cu_rows + seq + 1), a.N), start = __ldg(a.start_pos + seq);
   const int slot = a.cache_slot ? __ldg(a.cache_slot + seq) : seq;
   if (row0 < 0 || row0 >= row1 || slot < 0 || slot >= a.n_slots) return;
-  // positions [pos0, pos1) of the slot are written, this CTA's [p0, p1) in one block
-  const int pos0 = max(start, 0);
-  const int pos1 = (int)min((long long)start + (row1 - row0), (long long)a.S_max);
-  const long long block0 = (long long)((pos0 >> a.shift) + (at - first_cta(seq))) << a.shift;
-  if (block0 >= pos1) return;
-  const int p0 = max((int)block0, pos0), p1 = (int)min((long long)pos1, block0 + (1 << a.shift));
-  const int count = p1 - p0, earlier = p0 - (int)block0;
+  AppendSpan span;
+  if (!append_span(at - first_cta(seq), start, row1 - row0, a.S_max, a.shift, &span)) return;
+  const int block0 = span.block0, p0 = span.p0, count = span.p1 - p0, earlier = p0 - block0;
   const __nv_bfloat16* kv = a.kv_new + ((long long)row0 + (p0 - (long long)start)) * kDl;
   const __nv_bfloat16* pe = a.pe_new + ((long long)row0 + (p0 - (long long)start)) * kDr;
   float* sp = a.kv_scale + (size_t)slot * a.n_blocks + (p0 >> a.shift);

@@ -831,6 +831,8 @@ int run_evict(const EvictBuffers& e, const int32_t* end_pos, int32_t* kept, int3
   // against one: 1 row of 4K 14.4 us and 13.4, of 8K 15.3 and 17.9; 8 rows of 8K
   // 15.3 and 18.1, of 32K 18.4 and 49.6; 16 rows of 8K 26.9 and 17.5, of 16K 29.3
   // and 29.4, of 32K 33.1 and 49.4; 32 rows of 32K (two rounds) 48.0 and 49.4.
+  // Rows 9 to 15 go by the 16-row figures, though eight CTAs would suit them
+  // earlier: 12 rows of 16384 28.1 (one CTA), of 16385 18.5 (eight).
   const int n_cta = B <= info->sm_count / kSelectCluster && S_max >= (B <= 8 ? 8192 : 16385) ? kSelectCluster : 1;
   if ((rc = launch_cluster(evict_select_kernel, (unsigned)n_cta, dim3((unsigned)(B * n_cta)), dim3(kSelectThreads), 0, stream, false,
                       static_cast<const float*>(e.in[0]), end_pos, static_cast<float*>(e.out[0]), kept, new_end, S_max,
