@@ -528,7 +528,8 @@ int mla_append_fp8(const void* kv_new, const void* pe_new, const int32_t* cu_row
  *   lse   f32 [B,n_heads], the decode step's lse_out
  *   acc   f32 [B,S_max], read and written at the selected positions only
  * A position's total gets one addition a call (valid indices are distinct), so
- * results are reproducible.  Scores and weights are f32, of the bf16 q_lat:
+ * results are reproducible.  Scores and weights are f32, of the bf16 q_lat
+ * (over the 8-bit cache what is below 2^-19 of a row's largest q_lat is lost):
  * weights of a row add up to the heads' number to within its rounding.  Returns
  * an mla_status.
  */

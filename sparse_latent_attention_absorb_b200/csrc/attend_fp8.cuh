@@ -24,7 +24,8 @@ namespace mla {
 // the second's sign), one more than bf16's, and 8-bit products run at twice the
 // rate of bf16 products: two of them cost what one bf16 product costs, and the
 // codes go to the tensor cores as they lie in the cache, with no conversion and
-// at half of bf16's shared memory.
+// at half of bf16's shared memory.  (The softmax weights' second number is E5M2,
+// for its range: eight bits.)
 //
 // An fp16 number f of magnitude below 1.8 has E4M3's exponent field for the
 // value 2^8 f, subnormals included, so rounding 2^8 f to E4M3 is rounding f's
@@ -161,7 +162,7 @@ __device__ __forceinline__ int query_exponent(float amax, float rmax) {
 // two of them took 4900 cycles a tile), 12 query load and QK issue, 13 TMEM and PV
 // issue, 14 positions, scales and L2 prefetch, 15 pushes.
 //
-// Measured (one B200, 64 rows of 2048 positions, 128 heads): 49 us, of which 10
+// Measured (one B200, 64 rows of 2048 positions, 128 heads): 50 us, of which 10
 // lie before the first and behind the last tile (set-up 1.5, the query 0.6 and
 // its limbs 2.5, the last tile's way to O 1.5, O to memory 1.9) and 2.4 us, 4500
 // cycles, are a tile's.  A tile's limits are 2340 cycles of MMA, about 2800 of

@@ -248,7 +248,9 @@ evict_select_kernel(const float* acc, const int32_t* __restrict__ end_pos, float
 //   out of place: a CTA per 128 (64) rows;
 //   in place: a cluster of eight CTAs per slot walks up its rows, and writes a
 //   step once all of it has been read (kept[i] >= i: what a step writes, no
-//   later step reads).
+//   later step reads).  Reads and writes take turns, and few slots leave SMs
+//   idle: whole calls 18.2, 75.8 and 121.0 us (1 row of 4096, 64 of up to 8192 in
+//   8 bits, 8 of 32768 in bf16) against 14.4, 50.6 and 64.0 out of place.
 constexpr int kMoveThreads = 512;
 // Rows of a warp, and of a CTA: out of place two CTAs share an SM, so that one
 // reads while the other writes, and bf16 rows then leave registers for four a
