@@ -464,10 +464,9 @@ int mla_output_projection_prepared(const void* x, const void* wo_prepared, void*
  * max|q_nope| max|W_UK| of a row, a head and 128 latent columns: where they all
  * lie 2^22 below that bound, they have bf16's digits, and fewer further down.)
  * The softmax weights enter the mix with eight significant bits, as bf16 weights
- * would, where weight times scale is at least 2^-7 of the largest of the same
- * 128 index slots; what is smaller is off by at most 2^-15 of that one or, if it
- * is more, of the mean of the sums of the 128-slot tiles so far (a tile's 128
- * together by 2^-8 of it).
+ * would, but no finer than 2^-15 of the largest (weight times its position's
+ * scale) of the same 128 index slots or, if it is more, of the mean of the sums
+ * of the 128-slot tiles so far (a tile's 128 together: 2^-8 of it).
  *
  * mla_sparse_attend_fp8: steps "scores" .. "mix" alone, as mla_sparse_attend
  * (o_part bf16 [R,n_split,n_heads,512], lse_part f32 [R,n_split,n_heads];

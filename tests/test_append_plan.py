@@ -84,6 +84,8 @@ def test_append_partition_is_exact(tmp_path):
 def test_append_leaves_out_rows_before_the_first_sequence_and_positions_behind_the_cache(block):
     """Row lists that begin behind row 0, and runs that begin behind the cache's end inside its last block, next to scales that
     are not set (0): exact, and nothing else is touched."""
+    from sparse_latent_attention_absorb_b200 import build
+    build.build()
     import torch
     from tests import cache8_refs as ref
     import sparse_latent_attention_absorb_b200 as mla

@@ -111,6 +111,8 @@ def test_buffers_are_made_under_the_calls_stream(host, name):
 @pytest.mark.parametrize("heads", [128, 16])
 def test_a_steps_buffers_are_not_handed_out_while_it_runs(heads):
     """A step on a side stream that starts late, while the current stream fills all the memory it can get again."""
+    from sparse_latent_attention_absorb_b200 import build
+    build.build()
     from tests import test_cache8 as t8
     g = t8.gen(3)
     c = t8.make_cache(g, 4, 400, 8)
